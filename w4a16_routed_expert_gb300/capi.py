@@ -1,4 +1,4 @@
-"""ctypes binding of include/moe_layer.h — argument marshalling only.
+"""ctypes binding of the headers in include/ — argument marshalling only.
 
 Every entry point has the same name as in the header. The library is loaded
 on first use; if it has not been built this raises instead of falling back
@@ -54,6 +54,31 @@ class moe_layer_profile_t(ctypes.Structure):
                 ("active_experts", ctypes.c_int32), ("tokens", ctypes.c_int32), ("single_launch", ctypes.c_int32)]
 
 
+# include/moe_attention.h
+MOE_DTYPE_F16, MOE_DTYPE_BF16 = 0, 1
+MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = 0, 1, 2, 3
+
+
+class moe_attn_config_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "dtype", "num_q_heads", "num_kv_heads", "head_dim", "max_tokens", "max_seqs", "rotary_dim",
+        "rope_interleaved", "rope_scaling", "rope_original_max_position")] + [(n, ctypes.c_double) for n in (
+        "rope_theta", "rope_factor", "rope_beta_fast", "rope_beta_slow", "norm_eps", "scale")] + [
+        ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in (
+        "num_pages", "page_stride", "slot_stride", "head_stride")]
+
+
+class moe_attn_buffers_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "q_norm", "k_norm")]
+
+
+class moe_attn_batch_t(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("q_offsets", ctypes.c_void_p),
+                ("max_q_len", ctypes.c_int32), ("seq_lens", ctypes.c_void_p), ("max_seq_len", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int32), ("prefix_len", ctypes.c_int32),
+                ("prefix_pages", ctypes.c_void_p), ("causal", ctypes.c_int32)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status
@@ -63,6 +88,7 @@ class MoEError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 # name -> (restype, argtypes)
 PROTOTYPES = {
@@ -91,6 +117,16 @@ PROTOTYPES = {
     "moe_layer_destroy": (_I32, [_P]),
     "moe_layer_last_error": (ctypes.c_char_p, [ctypes.c_void_p]),
     "moe_route_topk_static": (_I32, [_P, _I32, _I32, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
+    # include/moe_attention.h
+    "moe_attn_frequencies": (_I32, [ctypes.POINTER(moe_attn_config_t), ctypes.POINTER(ctypes.c_double),
+                                    ctypes.POINTER(ctypes.c_double)]),
+    "moe_attn_create": (_I32, [ctypes.POINTER(moe_attn_config_t), ctypes.POINTER(moe_attn_buffers_t),
+                               ctypes.POINTER(_P)]),
+    "moe_attn_rotate": (_I32, [_P, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _P, _I64, _P]),
+    "moe_attn_append": (_I32, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P]),
+    "moe_attn_forward": (_I32, [_P, _P, _I64, ctypes.POINTER(moe_attn_batch_t), _P, _I64, _P, _P]),
+    "moe_attn_sync": (_I32, [_P, _P]),
+    "moe_attn_destroy": (_I32, [_P]),
     # include/moe_residency.h
     "moe_slot_planner_create": (_P, [_I32, _I32]),
     "moe_slot_planner_plan": (_I32, [_P, ctypes.POINTER(_I32), _I32, _I32, ctypes.POINTER(_I32),

@@ -1,0 +1,72 @@
+// Device helpers shared by the attention operators' kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace moe {
+
+// The two 16-bit types: a pair of values in a 32-bit word, low half first.
+template <typename T>
+struct Half16;
+template <>
+struct Half16<__half> {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+};
+template <>
+struct Half16<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+};
+
+// Sequence b's query tokens, clamped to the batch: [*t0, *t0 + return).
+__device__ __forceinline__ int seq_tokens(const AttnArgs& a, int b, int* t0) {
+  const int lo = __ldg(a.q_offsets + b), hi = __ldg(a.q_offsets + b + 1);
+  const int n = hi - lo;
+  if (lo < 0 || hi > a.T || n < 0 || n > a.max_q_len) {
+    record_error(a.err, kAttnErrBounds);
+    *t0 = min(max(lo, 0), a.T);
+    return min(min(max(n, 0), a.max_q_len), a.T - *t0);
+  }
+  *t0 = lo;
+  return n;
+}
+// Sequence b's own keys, clamped to the bound the caller gave.
+__device__ __forceinline__ int seq_keys(const AttnArgs& a, int b) {
+  const int n = __ldg(a.seq_lens + b);
+  if (n < 0 || n > a.max_seq_len) {
+    record_error(a.err, kAttnErrBounds);
+    return min(max(n, 0), a.max_seq_len);
+  }
+  return n;
+}
+// A page of the cache, clamped to it.
+__device__ __forceinline__ int page_in_cache(const AttnArgs& a, int page) {
+  if ((unsigned)page >= (unsigned)a.num_pages) {
+    record_error(a.err, kAttnErrBounds);
+    return 0;
+  }
+  return page;
+}
+// Own keys that query token i of n sees when its sequence holds `keys`.
+__device__ __forceinline__ int keys_seen(const AttnArgs& a, int keys, int n, int i) {
+  return a.causal ? min(keys, max(0, keys - n + i + 1)) : keys;
+}
+
+}  // namespace moe
