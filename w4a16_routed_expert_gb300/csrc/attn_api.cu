@@ -25,6 +25,16 @@ struct moe_attn {
   void* ws = nullptr;
   uint32_t* err = nullptr;
   uint64_t* freq = nullptr;
+  // forward's workspace
+  int32_t* seq_of = nullptr;     // [max_tokens]
+  long long* share = nullptr;    // [2]
+  int32_t* own_off[2] = {};      // [max_seqs + 1]
+  float* part_o = nullptr;       // [part_rows][DP]
+  float2* part_ml = nullptr;     // [part_rows]
+  size_t part_rows = 0;
+  int DP = 0;
+  int box_rows = 0;              // slots of a copy of the few-row kernel
+  CUtensorMap rows_k, rows_v;
 };
 
 namespace {
@@ -171,6 +181,36 @@ void fill_rope(const moe_attn* h, moe::RopeArgs* a) {
   a->err = h->err;
 }
 
+// Enqueue a forward whose arguments have been checked.
+moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
+  const char* fn = "moe_attn_forward";
+  const bool bf16 = h->cfg.dtype == MOE_DTYPE_BF16;
+  const int own_rows = a.max_seq_len > 0 ? a.max_q_len * a.g : 0;
+  const int prefix_rows = a.prefix_len > 0 ? (int)std::min<long long>((long long)a.T * a.g, INT_MAX / 2) : 0;
+  moe::JoinArgs j = {};
+  j.a = a;
+  j.DP = h->DP;
+  if (own_rows || prefix_rows) {
+    const int rows = std::max(own_rows, prefix_rows);
+    const moe::AttnRowsPlan p = moe::plan_attn_rows(a.D, std::min(rows, moe::kRowsMax), a.B, h->num_sms);
+    moe::LineArgs& ln = j.line[0];
+    ln.row_block = rows <= 16 ? 16 : moe::kRowsMax;
+    ln.key_tile = moe::kRowsKeyTile;
+    ln.has_prefix = prefix_rows > 0;
+    ln.has_own = own_rows > 0;
+    ln.n_cta = p.n_cta;
+    ln.part_rows = std::min(rows, ln.row_block);
+    ln.share = h->share;
+    ln.own_off = h->own_off[0];
+    ln.part_o = h->part_o;
+    ln.part_ml = h->part_ml;
+    const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, ln, p, h->box_rows, bf16, false, s, h->pdl);
+    if (e != cudaSuccess) return cuda_error(e, fn);
+  }
+  const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -204,8 +244,28 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
     delete h;
     return cuda_error(e, "device query");
   }
-  // workspace: error word, frequencies
-  const size_t bytes = align256(4) + align256(64 * 8);
+  // workspace: error word, frequencies; with a cache the forward's tables and
+  // the blocks' partial rows
+  size_t bytes = align256(4) + align256(64 * 8);
+  const size_t S = (size_t)config->max_seqs + 1, N = (size_t)config->max_tokens;
+  if (buffers->k_cache) {
+    h->DP = config->head_dim <= 64 ? 64 : 128;
+    h->part_rows = 2 * N * config->num_q_heads + (size_t)h->num_sms * 2 * moe::kRowsMax;
+    bytes += align256(N * 4) + align256(2 * 8) + 2 * align256(S * 4) + align256(h->part_rows * h->DP * 4) +
+             align256(h->part_rows * 8);
+    h->box_rows = 16;  // the largest box that pages divide into
+    while (h->box_rows < moe::kRowsKeyTile && config->page_size % (2 * h->box_rows) == 0) h->box_rows *= 2;
+    const bool bf16 = config->dtype == MOE_DTYPE_BF16;
+    auto map = [&](CUtensorMap* tm, const void* cache, int slots, bool whole) {
+      return moe::encode_cache_map(tm, cache, bf16, config->head_dim, config->page_size, config->num_kv_heads,
+                                   config->num_pages, config->page_stride, config->slot_stride, config->head_stride,
+                                   slots, whole);
+    };
+    if (!map(&h->rows_k, buffers->k_cache, h->box_rows, true) || !map(&h->rows_v, buffers->v_cache, h->box_rows, true)) {
+      delete h;
+      return set_error(MOE_ERR_UNSUPPORTED, "the cache's shape and strides make no tensor map");
+    }
+  }
   e = cudaMalloc(&h->ws, bytes);
   if (e != cudaSuccess) {
     delete h;
@@ -216,6 +276,19 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   h->err = reinterpret_cast<uint32_t*>(p);
   p += align256(4);
   h->freq = reinterpret_cast<uint64_t*>(p);
+  p += align256(64 * 8);
+  if (buffers->k_cache) {
+    auto carve = [&](size_t b) {
+      char* at = p;
+      p += align256(b);
+      return at;
+    };
+    h->seq_of = reinterpret_cast<int32_t*>(carve(N * 4));
+    h->share = reinterpret_cast<long long*>(carve(2 * 8));
+    for (int i = 0; i < 2; ++i) h->own_off[i] = reinterpret_cast<int32_t*>(carve(S * 4));
+    h->part_o = reinterpret_cast<float*>(carve(h->part_rows * h->DP * 4));
+    h->part_ml = reinterpret_cast<float2*>(carve(h->part_rows * 8));
+  }
   uint64_t turns[64] = {};
   if (config->rotary_dim > 0) {
     double f[64], m;
@@ -227,7 +300,8 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
       turns[i] = t < 18446744073709551615.0 ? (uint64_t)t : 0;
     }
   }
-  e = cudaMemset(h->ws, 0, bytes);
+  // the small words and tables; partial rows are written before they are read
+  e = cudaMemset(h->ws, 0, h->part_o ? (size_t)((char*)h->part_o - (char*)h->ws) : bytes);
   if (e == cudaSuccess) e = cudaMemcpy(h->freq, turns, sizeof(turns), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
@@ -352,6 +426,10 @@ moe_status_t moe_attn_forward(moe_attn_t* h, const void* q, int64_t q_stride, co
   if (b->prefix_len > 0 && !b->prefix_pages)
     return set_error(MOE_ERR_INVALID_ARG, "%s: prefix_pages must not be NULL", fn);
   if (b->causal != 0 && b->causal != 1) return set_error(MOE_ERR_INVALID_ARG, "%s: causal must be 0 or 1", fn);
+  // tiles of one key head, counted in 32 bits on the device
+  const long long blocks = ((long long)b->max_q_len * (c.num_q_heads / c.num_kv_heads) + 15) / 16;
+  if ((b->max_seq_len + moe::kRowsKeyTile - 1LL) / moe::kRowsKeyTile * blocks > (1LL << 30) / b->num_seqs)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs * max_q_len * max_seq_len is more than one call takes", fn);
   st = check_rows(h, fn, "q", q, q_stride, c.num_q_heads);
   if (st == MOE_OK) st = check_rows(h, fn, "out", out, out_stride, c.num_q_heads);
   if (st != MOE_OK) return st;
@@ -385,8 +463,8 @@ moe_status_t moe_attn_forward(moe_attn_t* h, const void* q, int64_t q_stride, co
   a.out_stride = out_stride;
   a.lse = lse;
   a.err = h->err;
-  const cudaError_t e = moe::launch_attn_simple(a, c.dtype == MOE_DTYPE_BF16, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+  a.seq_of = h->seq_of;
+  return forward(h, a, static_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_attn_sync(moe_attn_t* h, void* stream) {
