@@ -100,6 +100,12 @@ AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms);
 cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              const AttnRowsPlan& plan, int box_slots, bool bf16, bool late_wait, cudaStream_t s, bool pdl);
 
+// Many rows to a key: 128-row tcgen05 tiles, two to a block, one block per SM.
+constexpr int kTileRows = 256;
+constexpr int kTileKeyTile = 128;
+cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
+                             int box_slots, bool bf16, cudaStream_t s, bool pdl);
+
 // Joins the partials of up to two kernels (n_cta = 0: not run) into out and lse.
 struct JoinArgs {
   AttnArgs a;

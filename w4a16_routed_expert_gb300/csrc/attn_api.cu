@@ -33,8 +33,8 @@ struct moe_attn {
   float2* part_ml = nullptr;     // [part_rows]
   size_t part_rows = 0;
   int DP = 0;
-  int box_rows = 0;              // slots of a copy of the few-row kernel
-  CUtensorMap rows_k, rows_v;
+  int box_rows = 0, box_tile = 0;  // slots of one copy of the few-row and of the tile kernel
+  CUtensorMap rows_k, rows_v, tile_k, tile_v;
 };
 
 namespace {
@@ -190,21 +190,38 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   moe::JoinArgs j = {};
   j.a = a;
   j.DP = h->DP;
-  if (own_rows || prefix_rows) {
-    const int rows = std::max(own_rows, prefix_rows);
-    const moe::AttnRowsPlan p = moe::plan_attn_rows(a.D, std::min(rows, moe::kRowsMax), a.B, h->num_sms);
-    moe::LineArgs& ln = j.line[0];
-    ln.row_block = rows <= 16 ? 16 : moe::kRowsMax;
-    ln.key_tile = moe::kRowsKeyTile;
-    ln.has_prefix = prefix_rows > 0;
-    ln.has_own = own_rows > 0;
-    ln.n_cta = p.n_cta;
-    ln.part_rows = std::min(rows, ln.row_block);
-    ln.share = h->share;
-    ln.own_off = h->own_off[0];
-    ln.part_o = h->part_o;
-    ln.part_ml = h->part_ml;
-    const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, ln, p, h->box_rows, bf16, false, s, h->pdl);
+  // Up to 32 rows to a key go to the few-row kernel (16-row tiles, no padding
+  // to speak of, two blocks an SM), more to the 128-row tiles of the tcgen05
+  // kernel, of which a block takes two.
+  const bool tile_own = own_rows > moe::kRowsMax, tile_prefix = prefix_rows > moe::kRowsMax || (tile_own && prefix_rows);
+  const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
+  size_t used = 0;
+  auto line = [&](int i, int row_block, int key_tile, int n_cta, bool prefix, bool own) {
+    moe::LineArgs& ln = j.line[i];
+    ln.row_block = row_block;
+    ln.key_tile = key_tile;
+    ln.has_prefix = prefix;
+    ln.has_own = own;
+    ln.n_cta = n_cta;
+    ln.part_rows = std::min(std::max(prefix ? prefix_rows : 0, own ? own_rows : 0), row_block);
+    ln.share = h->share + i;
+    ln.own_off = h->own_off[i];
+    ln.part_o = h->part_o + used * h->DP;
+    ln.part_ml = h->part_ml + used;
+    used += (size_t)moe::line_part_rows(ln, a.T, a.Hq);
+  };
+  if (tile_own || tile_prefix) {
+    line(0, moe::kTileRows, moe::kTileKeyTile, h->num_sms, tile_prefix, tile_own);
+    const cudaError_t e = moe::launch_attn_tile(h->tile_k, h->tile_v, a, j.line[0], h->box_tile, bf16, s, h->pdl);
+    if (e != cudaSuccess) return cuda_error(e, fn);
+  }
+  if (few_own || few_prefix) {
+    const int rows = std::max(few_own ? own_rows : 0, few_prefix ? prefix_rows : 0);
+    const moe::AttnRowsPlan p = moe::plan_attn_rows(a.D, rows, a.B, h->num_sms);
+    line(1, rows <= 16 ? 16 : moe::kRowsMax, moe::kRowsKeyTile, p.n_cta, few_prefix, few_own);
+    // behind the tile kernel it need not wait for its results, only not end before it
+    const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, j.line[1], p, h->box_rows, bf16,
+                                                tile_prefix && h->pdl, s, h->pdl);
     if (e != cudaSuccess) return cuda_error(e, fn);
   }
   const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
@@ -250,18 +267,21 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   const size_t S = (size_t)config->max_seqs + 1, N = (size_t)config->max_tokens;
   if (buffers->k_cache) {
     h->DP = config->head_dim <= 64 ? 64 : 128;
-    h->part_rows = 2 * N * config->num_q_heads + (size_t)h->num_sms * 2 * moe::kRowsMax;
+    h->part_rows = 2 * N * config->num_q_heads + (size_t)h->num_sms * (2 * moe::kRowsMax + moe::kTileRows);
     bytes += align256(N * 4) + align256(2 * 8) + 2 * align256(S * 4) + align256(h->part_rows * h->DP * 4) +
              align256(h->part_rows * 8);
     h->box_rows = 16;  // the largest box that pages divide into
     while (h->box_rows < moe::kRowsKeyTile && config->page_size % (2 * h->box_rows) == 0) h->box_rows *= 2;
+    h->box_tile = h->box_rows;
+    while (h->box_tile < moe::kTileKeyTile && config->page_size % (2 * h->box_tile) == 0) h->box_tile *= 2;
     const bool bf16 = config->dtype == MOE_DTYPE_BF16;
     auto map = [&](CUtensorMap* tm, const void* cache, int slots, bool whole) {
       return moe::encode_cache_map(tm, cache, bf16, config->head_dim, config->page_size, config->num_kv_heads,
                                    config->num_pages, config->page_stride, config->slot_stride, config->head_stride,
                                    slots, whole);
     };
-    if (!map(&h->rows_k, buffers->k_cache, h->box_rows, true) || !map(&h->rows_v, buffers->v_cache, h->box_rows, true)) {
+    if (!map(&h->rows_k, buffers->k_cache, h->box_rows, true) || !map(&h->rows_v, buffers->v_cache, h->box_rows, true) ||
+        !map(&h->tile_k, buffers->k_cache, h->box_tile, false) || !map(&h->tile_v, buffers->v_cache, h->box_tile, false)) {
       delete h;
       return set_error(MOE_ERR_UNSUPPORTED, "the cache's shape and strides make no tensor map");
     }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "attn_dev.cuh"
+#include "tc.cuh"
 
 namespace moe {
 
@@ -50,6 +51,48 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// ---- tcgen05 (tensor memory) beside tc.cuh
+// Instruction descriptor of kind::f16 with FP32 accumulation: M x N, A and B
+// both FP16 or both BF16, A K-major; B K-major, or with its rows along K
+// (b_rows_k: B is stored [k][n] with n contiguous).
+__host__ __device__ constexpr uint32_t attn_idesc(int M, int N, bool bf16, bool b_rows_k) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_rows_k ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Shared-memory descriptor of a [k][n] operand, n contiguous in 64-element
+// (128-byte) swizzled rows: 8-row groups 1024 bytes apart, the 64-wide column
+// blocks `col_block` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t saddr, uint32_t col_block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(col_block >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+// D[tmem] (+)= A[smem] B[smem], issued by one thread.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // 2^x, within 2^-22 relative; 2^-inf = 0
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

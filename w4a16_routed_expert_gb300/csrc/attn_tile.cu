@@ -1,0 +1,468 @@
+// Attention for many query rows to a key, on the 5th-generation tensor cores:
+// a prefix shared by a batch, chunks of prompt.
+//
+// A block takes up to 256 rows of a group as two tiles of 128 (a row is a
+// query token and one of the g query heads of a key head) over a run of its
+// keys, 128 at a time: S = Q K^T into tensor memory, running softmax in
+// registers (a thread a row), the probabilities back to tensor memory as the
+// A operand of O += P V, whose accumulator stays in tensor memory. Per SM a
+// key tile costs 4 products of 128 x 128 x 128 (~2100 cycles at the measured
+// peak for two row tiles) and 64 KB of keys and values (~2800 cycles at the
+// measured copy rate): up to ~190 rows the keys' bytes bound it, above that
+// the products.
+//
+// Warp roles (one block per SM):
+//   warps 0-3, 4-7  softmax of row tile 0, 1 (a warp reaches the 32 lanes of
+//                   tensor memory of its number mod 4); queries in, output out
+//   warp 8          TMA: pages to shared memory, 128-byte swizzle, keys and
+//                   values in turn through one ring
+//   warp 9          tensor memory and the single thread that issues the MMAs:
+//                   P V of a tile, then the next Q K^T of the same rows, so
+//                   that one row tile's products run under the other's softmax
+// Tensor memory: two S tiles (P takes the first half of S's columns) and two
+// output tiles, 512 columns at head size 128.
+//
+// MMAs of one thread run in order, so Q K^T of the next tile may overwrite
+// the columns that the P V issued just before it reads; and a completed
+// Q K^T means the P V before it has completed, so the softmax warps may
+// rescale the output without another barrier.
+#include "attn_line.cuh"
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kKT = kTileKeyTile;
+constexpr int kThreads = 12 * 32;  // three warpgroups: two of softmax, one of copies and MMAs
+constexpr int kWarpCopy = 8, kWarpMma = 9;
+constexpr int kMaxStages = 8;
+
+struct SmemPlan {
+  uint32_t ring, bars, misc, off, bytes;
+};
+__host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
+  SmemPlan p;
+  p.ring = 2u * 128 * DP * 2;  // after the queries
+  p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
+  p.misc = p.bars + (2 * kMaxStages + 9) * 8;
+  p.misc = (p.misc + 15) & ~15u;
+  p.off = p.misc + 64;
+  p.bytes = p.off + (uint32_t)(B + 1) * 4;
+  return p;
+}
+
+struct Misc {
+  uint32_t tmem;
+  int abort_flag;
+  int issued;      // stages handed to TMA
+  int mma_issued;
+  int32_t scratch[12];
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
+                const LineArgs ln, int stages, int box_log2) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  constexpr int NH = DP / 64;
+  constexpr bool kBf16 = sizeof(T) == 2 && ProbBias<T>::value == 0.f;
+  constexpr uint32_t kHalf = 128 * 128;             // bytes of 64 elements of 128 rows
+  constexpr uint32_t kTileBytes = NH * kHalf;       // a query, key or value tile
+  const SmemPlan sp = smem_plan(DP, stages, a.B);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* q_full = empty + kMaxStages;  // [2] queries in shared memory and the output tile drained
+  uint64_t* s_full = q_full + 2;          // [2] logits in tensor memory
+  uint64_t* p_full = s_full + 2;          // [2] probabilities in tensor memory
+  uint64_t* o_full = p_full + 2;          // [2] output complete
+  uint64_t* drain = o_full + 2;
+  Misc* misc = reinterpret_cast<Misc*>(smem + sp.misc);
+  int32_t* own_off = reinterpret_cast<int32_t*>(smem + sp.off);
+  volatile int* abort_flag = &misc->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 4);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(drain, 1);
+    misc->abort_flag = 0;
+    misc->issued = 0;
+    misc->mma_issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpCopy && lane == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  if (warp == kWarpMma) tmem_alloc(&misc->tmem, 512);
+  pdl_wait();
+  // only now: a kernel that starts on this trigger and does not wait itself
+  // may rely on everything before this launch
+  pdl_trigger();
+  const int own_total = scan_own<kThreads>(a, ln, own_off, misc->scratch);
+  long long total;
+  const long long share = line_share(a, ln, own_off, own_total, &total);
+  const long long x0 = min(share * blockIdx.x, total), x1 = min(x0 + share, total);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+
+  // registers: 168 a thread at launch; a softmax thread holds 128 logits, and
+  // 2 x 208 + 88 = 3 x 168
+  if (warp >= kWarpCopy) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == kWarpCopy) {
+    // --------------------------------------------------------------- copies
+    // lane (box, half of the head): one box of every key and value tile
+    const int c = lane / NH, hf = lane % NH;
+    const int box = 1 << box_log2;
+    const bool mine = c < (kKT >> box_log2);
+    const bool split = (a.D & 63) != 0;
+    const int cx = split ? hf * 64 : 0, ch = split ? 0 : hf;
+    int st = 0, issued = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok;) {
+      const Segment s = segment_at(a, ln, own_off, x, x1);
+      const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      auto page_of = [&](int tile) {
+        const int key = tile * kKT + (c << box_log2);
+        return mine && key < s.nkeys ? page_in_cache(a, __ldg(tab + key / a.page_size)) : -1;
+      };
+      int page = page_of(s.tile);
+      for (int i = 0; i < s.tiles && ok; ++i) {
+        const int tile = s.tile + i;
+        const int next = i + 1 < s.tiles ? page_of(tile + 1) : -1;
+        const int boxes = (min(kKT, max(0, s.nkeys - tile * kKT)) + box - 1) >> box_log2;
+        const int slot = (tile * kKT + (c << box_log2)) % a.page_size;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const bool got = mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_5d(smem_u32(smem) + sp.ring + (uint32_t)st * kTileBytes + (uint32_t)hf * kHalf +
+                            (uint32_t)c * box * 128,
+                        kv ? &tv : &tk, cx, slot, ch, s.h, page, &full[st]);
+          ++issued;
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        page = next;
+      }
+      x += s.tiles;
+    }
+    if (lane == 0) misc->issued = issued;
+  } else if (warp == kWarpMma) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_s = attn_idesc(128, kKT, kBf16, false);
+      constexpr uint32_t id_o = attn_idesc(128, DP, kBf16, true);
+      const uint32_t ring = smem_u32(smem) + sp.ring;
+      int st = 0;
+      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.err); };
+      auto step = [&]() {
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      auto qk = [&](int t, int stage) {
+        const uint32_t qa = smem_u32(smem) + (uint32_t)t * kTileBytes, kb = ring + (uint32_t)stage * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32;
+          mma_f16_ss(tmem + t * 128, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), id_s, k > 0);
+        }
+        misc->mma_issued = 1;
+        mma_commit(&s_full[t]);
+      };
+      bool ok = true;
+      for (long long x = x0; x < x1 && ok;) {
+        const Segment s = segment_at(a, ln, own_off, x, x1);
+        const int nt = s.rows > 128 ? 2 : 1;
+        ok = wait(&full[st], ph);
+        for (int t = 0; t < nt && ok; ++t) {
+          ok = wait(&q_full[t], qph[t]);
+          qph[t] ^= 1u;
+          if (!ok) break;
+          tc_fence_after();
+          qk(t, st);
+        }
+        if (!ok) break;
+        mma_commit(&empty[st]);
+        step();
+        for (int i = 0; i < s.tiles && ok; ++i) {
+          const int vst = st;
+          ok = wait(&full[st], ph);
+          if (!ok) break;
+          step();
+          const bool more = i + 1 < s.tiles;
+          for (int t = 0; t < nt; ++t) {
+            ok = wait(&p_full[t], pph[t]);
+            pph[t] ^= 1u;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vb = ring + (uint32_t)vst * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kKT / 16; ++k)
+              mma_f16_ts(tmem + 256 + t * DP, tmem + t * 128 + k * 8, smem_desc_rows_k(vb + (uint32_t)k * 2048, kHalf),
+                         id_o, (i > 0 || k > 0) ? 1u : 0u);
+            if (!more) {
+              mma_commit(&o_full[t]);
+              continue;
+            }
+            if (t == 0) {
+              ok = wait(&full[st], ph);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            qk(t, st);
+          }
+          if (!ok) break;
+          mma_commit(&empty[vst]);
+          if (more) {
+            mma_commit(&empty[st]);
+            step();
+          }
+        }
+        x += s.tiles;
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------- softmax
+    const int t = warp >> 2;                       // row tile
+    const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the group
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * DP;
+    const float sc = a.scale * 1.44269504088896340736f;
+    unsigned char* qtile = smem + (uint32_t)t * kTileBytes;
+    const int rl = r & 127;
+    auto load_q = [&](const Segment& s) {
+      const bool valid = r < s.rows;
+      const int row = s.row0 + r, tok = s.t0 + row / a.g, hq = s.h * a.g + row % a.g;
+      const T* src = static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (long long)hq * a.D;
+#pragma unroll
+      for (int c8 = 0; c8 < DP / 8; ++c8) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (valid && c8 * 8 < a.D) v = *reinterpret_cast<const uint4*>(src + c8 * 8);
+        *reinterpret_cast<uint4*>(qtile + (uint32_t)(c8 >> 3) * kHalf + (uint32_t)rl * 128 +
+                                  (uint32_t)(((c8 & 7) ^ (rl & 7)) << 4)) = v;
+      }
+      fence_async_smem();
+    };
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    uint32_t sph = 0, oph = 0;
+    long long idx = 0;  // ring position of the segment's first key tile
+    Segment s;
+    if (x0 < x1) {
+      s = segment_at(a, ln, own_off, x0, x1);
+      if (t == 0 || s.rows > 128) {
+        load_q(s);
+        arrive(&q_full[t]);
+      }
+    }
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok;) {
+      const bool used = t == 0 || s.rows > 128;
+      const bool any_row = t * 128 + (warp & 3) * 32 < s.rows;  // this warp has a row
+      float mref = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      if (used) {
+        const int row = s.row0 + min(r, s.rows - 1);
+        const int lim = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
+        const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
+        for (int i = 0; i < s.tiles; ++i) {
+          const int k0 = (s.tile + i) * kKT;
+          const bool got = mbar_wait(&s_full[t], sph, abort_flag, a.err);
+          sph ^= 1u;
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (any_row) {
+            uint32_t sr[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, sr[c]);
+            tmem_ld_wait();
+            if (k0 + kKT > all_see) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (k0 + c * 32 + e >= lim) sr[c][e] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              mx[c] = __uint_as_float(sr[c][0]);
+#pragma unroll
+              for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][e]));
+            }
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            if (__any_sync(0xffffffffu, m > mref + kLazy)) {
+              const float mn = fmaxf(mref, m);
+              const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
+              mref = mn;
+              l2.x *= f;
+              l2.y *= f;
+              if (i > 0) {
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                  uint32_t o[32];
+                  tmem_ld32(to + c * 32, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st32(to + c * 32, o);
+                }
+              }
+            }
+            const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
+            const float2 sc2 = make_float2(sc, sc), nref = make_float2(-ref, -ref);
+#pragma unroll
+            for (int hs = 0; hs < 2; ++hs) {
+              uint32_t p[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int c = hs * 2 + (e >> 4), w = (e & 15) * 2;
+                float2 v = ffma2(make_float2(__uint_as_float(sr[c][w]), __uint_as_float(sr[c][w + 1])), sc2, nref);
+                v.x = exp2_fast(v.x);
+                v.y = exp2_fast(v.y);
+                l2 = fadd2(l2, v);
+                p[e] = Half16<T>::pack(v.x, v.y);
+              }
+              tmem_st32(ts + hs * 32, p);
+            }
+            tmem_st_wait();
+          }
+          if (s.nkeys - k0 < kKT) {
+            // slots past the end may hold anything: their values become zeros
+            // (a zero weight would not stop a NaN)
+            const long long at = idx + 2 * i + 1;
+            const int vst = (int)(at % stages);
+            const bool there = mbar_wait(&full[vst], (uint32_t)(at / stages) & 1u, abort_flag, a.err);
+            if (!__all_sync(0xffffffffu, there)) {
+              ok = false;
+              break;
+            }
+            const int here = max(0, s.nkeys - k0);
+            unsigned char* vt = smem + sp.ring + (uint32_t)vst * kTileBytes;
+            for (int z = tid & 127; z < (kKT - here) * (DP / 8); z += 128) {
+              const int zr = here + z / (DP / 8), c8 = z % (DP / 8);
+              *reinterpret_cast<uint4*>(vt + (uint32_t)(c8 >> 3) * kHalf + (uint32_t)zr * 128 +
+                                        (uint32_t)((c8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+          }
+          tc_fence_before();
+          arrive(&p_full[t]);
+        }
+      }
+      if (!ok) break;
+      const Segment cur = s;
+      x += s.tiles;
+      idx += 2 * (long long)s.tiles;
+      bool next_used = false;
+      if (x < x1) {
+        // the last Q K^T of this part has completed: its queries' place is free
+        s = segment_at(a, ln, own_off, x, x1);
+        next_used = t == 0 || s.rows > 128;
+        if (next_used) load_q(s);
+      }
+      if (used) {
+        const bool got = mbar_wait(&o_full[t], oph, abort_flag, a.err);
+        oph ^= 1u;
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any_row) {
+          float* dst = ln.part_o + (cur.prow + r) * DP;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
+            if (r < cur.rows) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(dst + c * 32 + e * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          if (r < cur.rows) ln.part_ml[cur.prow + r] = make_float2(mref, l2.x + l2.y);
+        }
+        tc_fence_before();
+      }
+      if (next_used) arrive(&q_full[t]);
+    }
+  }
+
+  // ------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (misc->abort_flag) {
+    // a block that gave up lets its copies and MMAs end before it leaves
+    if (warp == kWarpCopy && lane == 0) {
+      const int n = misc->issued;
+      for (int i = 0; i < stages && i < n; ++i)
+        mbar_wait(&full[i], (uint32_t)((n - 1 - i) / stages) & 1u, nullptr, nullptr);
+    }
+    if (warp == kWarpMma && lane == 0 && misc->mma_issued) {
+      mma_commit(drain);
+      mbar_wait(drain, 0, nullptr, nullptr);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int DP>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
+                   cudaStream_t s, bool pdl) {
+  int stages = kMaxStages;  // as many as fit
+  while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
+  const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
+  const cudaError_t e = ensure_smem(k_attn_tile<T, DP>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_attn_tile<T, DP>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages, box_log2);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
+                             int box_slots, bool bf16, cudaStream_t s, bool pdl) {
+  int bl = 4;
+  while ((1 << bl) < box_slots) ++bl;
+  if (a.D <= 64)
+    return bf16 ? launch<__nv_bfloat16, 64>(tk, tv, a, ln, bl, s, pdl) : launch<__half, 64>(tk, tv, a, ln, bl, s, pdl);
+  return bf16 ? launch<__nv_bfloat16, 128>(tk, tv, a, ln, bl, s, pdl) : launch<__half, 128>(tk, tv, a, ln, bl, s, pdl);
+}
+
+}  // namespace moe
