@@ -50,7 +50,6 @@ struct AttnArgs {
   const int32_t *q_offsets, *seq_lens, *block_table, *prefix_pages;
   int table_stride, prefix_len, causal, max_q_len, max_seq_len;
   float scale;           // of the logits
-  int32_t* seq_of;       // workspace [T]: each token's sequence
   void* out;
   long long out_stride;
   float* lse;            // nullable
@@ -61,26 +60,34 @@ struct AttnArgs {
 // `row_block` query rows reads (a row is a query token and one of the g query
 // heads of a key head) form a group of key tiles: per key head and row block
 // of all tokens the prefix's tiles, then per sequence, key head and row block
-// the own keys'. All groups' tiles stand in one line, and each of n_cta
-// blocks takes an equal run of it, so the work is even whatever the lengths.
-// A block's run within one group gives one partial result (running maximum,
-// sum, unnormalised output rows); the rows' partials are joined by
-// launch_attn_join.
+// the own keys'. All groups stand in one line, each as its tiles after
+// `weight` empty places (what starting on a group costs, in tiles), and each
+// of n_cta blocks takes an equal run of it, so the work is even whatever the
+// lengths. A block's run within one group gives one partial result (running
+// maximum, sum, unnormalised output rows); launch_attn_join joins the rows'
+// partials. Places are counted in 32 bits; the host checks that they fit.
 struct LineArgs {
   int row_block;         // rows of a group at most
   int key_tile;          // keys of a tile
+  int weight;
   int has_prefix, has_own;
   int n_cta;
   int part_rows;         // rows a partial takes at most: min(row_block, most rows of a group)
-  // device workspace, written by the kernel's first block for the join
-  long long* share;      // tiles per block
-  int32_t* own_off;      // [B + 1] own tiles of one key head before each sequence
-  float* part_o;         // [rows][DP]: a group's rows at its first row + block * part_rows
+  int part_row0;         // this kernel's first row of partials
+  float* part_o;         // [rows][DP]: block c's partial of a group stands at the group's first row + c * part_rows
   float2* part_ml;       // [rows] maximum (log2 units), sum
+  int2 *info_prefix, *info_own;  // [T][Hq] first partial row and number of partials, 0 between forwards
 };
 // Rows of partial results one kernel can write.
 inline long long line_part_rows(const LineArgs& ln, long long T, long long Hq) {
   return (ln.has_prefix + ln.has_own) * T * Hq + (long long)ln.n_cta * ln.part_rows;
+}
+// Most places the line can have.
+inline long long line_places(const AttnArgs& a, const LineArgs& ln) {
+  const long long rows = (long long)a.T * a.g, kt = ln.key_tile, rb = ln.row_block;
+  const long long prefix = ln.has_prefix ? (rows + rb - 1) / rb * ((a.prefix_len + kt - 1) / kt + ln.weight) : 0;
+  const long long own = ln.has_own ? (rows / rb + a.B) * ((a.max_seq_len + kt - 1) / kt + ln.weight) : 0;
+  return (prefix + own) * a.Hk;
 }
 
 // Tensor maps of one cache tensor: boxes of `slots` slots x 64 elements, or of
@@ -97,19 +104,24 @@ struct AttnRowsPlan {
   size_t smem;
 };
 AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms);
+constexpr int kRowsWeight = 2;   // LineArgs::weight
 cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              const AttnRowsPlan& plan, int box_slots, bool bf16, bool late_wait, cudaStream_t s, bool pdl);
 
 // Many rows to a key: 128-row tcgen05 tiles, two to a block, one block per SM.
 constexpr int kTileRows = 256;
 constexpr int kTileKeyTile = 128;
+constexpr int kTileWeight = 2;   // LineArgs::weight
 cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              int box_slots, bool bf16, cudaStream_t s, bool pdl);
 
-// Joins the partials of up to two kernels (n_cta = 0: not run) into out and lse.
+// Joins the partials of a forward into out and lse.
 struct JoinArgs {
   AttnArgs a;
-  LineArgs line[2];
+  const float* part_o;
+  const float2* part_ml;
+  int2 *info_prefix, *info_own;
+  int prefix_step, own_step;  // rows between the partials of one row (0: that kind was not computed)
   int DP;
 };
 cudaError_t launch_attn_join(const JoinArgs& j, bool bf16, cudaStream_t s, bool pdl);

@@ -26,9 +26,7 @@ struct moe_attn {
   uint32_t* err = nullptr;
   uint64_t* freq = nullptr;
   // forward's workspace
-  int32_t* seq_of = nullptr;     // [max_tokens]
-  long long* share = nullptr;    // [2]
-  int32_t* own_off[2] = {};      // [max_seqs + 1]
+  int2* info[2] = {};            // [max_tokens][Hq] of the prefix, of own keys: where a row's partials are
   float* part_o = nullptr;       // [part_rows][DP]
   float2* part_ml = nullptr;     // [part_rows]
   size_t part_rows = 0;
@@ -187,41 +185,57 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   const bool bf16 = h->cfg.dtype == MOE_DTYPE_BF16;
   const int own_rows = a.max_seq_len > 0 ? a.max_q_len * a.g : 0;
   const int prefix_rows = a.prefix_len > 0 ? (int)std::min<long long>((long long)a.T * a.g, INT_MAX / 2) : 0;
-  moe::JoinArgs j = {};
-  j.a = a;
-  j.DP = h->DP;
   // Up to 32 rows to a key go to the few-row kernel (16-row tiles, no padding
   // to speak of, two blocks an SM), more to the 128-row tiles of the tcgen05
   // kernel, of which a block takes two.
   const bool tile_own = own_rows > moe::kRowsMax, tile_prefix = prefix_rows > moe::kRowsMax || (tile_own && prefix_rows);
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
-  size_t used = 0;
-  auto line = [&](int i, int row_block, int key_tile, int n_cta, bool prefix, bool own) {
-    moe::LineArgs& ln = j.line[i];
-    ln.row_block = row_block;
-    ln.key_tile = key_tile;
-    ln.has_prefix = prefix;
-    ln.has_own = own;
-    ln.n_cta = n_cta;
-    ln.part_rows = std::min(std::max(prefix ? prefix_rows : 0, own ? own_rows : 0), row_block);
-    ln.share = h->share + i;
-    ln.own_off = h->own_off[i];
-    ln.part_o = h->part_o + used * h->DP;
-    ln.part_ml = h->part_ml + used;
-    used += (size_t)moe::line_part_rows(ln, a.T, a.Hq);
+  moe::JoinArgs j = {};
+  j.a = a;
+  j.DP = h->DP;
+  j.part_o = h->part_o;
+  j.part_ml = h->part_ml;
+  j.info_prefix = h->info[0];
+  j.info_own = h->info[1];
+  long long used = 0;
+  auto line = [&](moe::LineArgs* ln, int row_block, int key_tile, int weight, int n_cta, bool prefix, bool own) {
+    ln->row_block = row_block;
+    ln->key_tile = key_tile;
+    ln->weight = weight;
+    ln->has_prefix = prefix;
+    ln->has_own = own;
+    ln->n_cta = n_cta;
+    ln->part_rows = std::min(std::max(prefix ? prefix_rows : 0, own ? own_rows : 0), row_block);
+    ln->part_row0 = (int)used;
+    ln->part_o = h->part_o;
+    ln->part_ml = h->part_ml;
+    ln->info_prefix = h->info[0];
+    ln->info_own = h->info[1];
+    used += moe::line_part_rows(*ln, a.T, a.Hq);
+    if (prefix) j.prefix_step = ln->part_rows;
+    if (own) j.own_step = ln->part_rows;
+    return moe::line_places(a, *ln) <= INT_MAX;
   };
-  if (tile_own || tile_prefix) {
-    line(0, moe::kTileRows, moe::kTileKeyTile, h->num_sms, tile_prefix, tile_own);
-    const cudaError_t e = moe::launch_attn_tile(h->tile_k, h->tile_v, a, j.line[0], h->box_tile, bf16, s, h->pdl);
-    if (e != cudaSuccess) return cuda_error(e, fn);
-  }
+  moe::LineArgs tile = {}, few = {};
+  moe::AttnRowsPlan plan = {};
+  bool fits = true;
+  if (tile_own || tile_prefix)
+    fits = line(&tile, moe::kTileRows, moe::kTileKeyTile, moe::kTileWeight, h->num_sms, tile_prefix, tile_own);
   if (few_own || few_prefix) {
     const int rows = std::max(few_own ? own_rows : 0, few_prefix ? prefix_rows : 0);
-    const moe::AttnRowsPlan p = moe::plan_attn_rows(a.D, rows, a.B, h->num_sms);
-    line(1, rows <= 16 ? 16 : moe::kRowsMax, moe::kRowsKeyTile, p.n_cta, few_prefix, few_own);
+    plan = moe::plan_attn_rows(a.D, rows, a.B, h->num_sms);
+    fits = line(&few, rows <= 16 ? 16 : moe::kRowsMax, moe::kRowsKeyTile, moe::kRowsWeight, plan.n_cta, few_prefix,
+                few_own) && fits;
+  }
+  if (!fits) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens and lengths beyond what one call takes", fn);
+  if (tile.n_cta) {
+    const cudaError_t e = moe::launch_attn_tile(h->tile_k, h->tile_v, a, tile, h->box_tile, bf16, s, h->pdl);
+    if (e != cudaSuccess) return cuda_error(e, fn);
+  }
+  if (few.n_cta) {
     // behind the tile kernel it need not wait for its results, only not end before it
-    const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, j.line[1], p, h->box_rows, bf16,
-                                                tile_prefix && h->pdl, s, h->pdl);
+    const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, few, plan, h->box_rows, bf16,
+                                                tile.n_cta && h->pdl, s, h->pdl);
     if (e != cudaSuccess) return cuda_error(e, fn);
   }
   const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
@@ -264,12 +278,11 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   // workspace: error word, frequencies; with a cache the forward's tables and
   // the blocks' partial rows
   size_t bytes = align256(4) + align256(64 * 8);
-  const size_t S = (size_t)config->max_seqs + 1, N = (size_t)config->max_tokens;
+  const size_t NR = (size_t)config->max_tokens * config->num_q_heads;
   if (buffers->k_cache) {
     h->DP = config->head_dim <= 64 ? 64 : 128;
-    h->part_rows = 2 * N * config->num_q_heads + (size_t)h->num_sms * (2 * moe::kRowsMax + moe::kTileRows);
-    bytes += align256(N * 4) + align256(2 * 8) + 2 * align256(S * 4) + align256(h->part_rows * h->DP * 4) +
-             align256(h->part_rows * 8);
+    h->part_rows = 2 * NR + (size_t)h->num_sms * (2 * moe::kRowsMax + moe::kTileRows);
+    bytes += 2 * align256(NR * 8) + align256(h->part_rows * h->DP * 4) + align256(h->part_rows * 8);
     h->box_rows = 16;  // the largest box that pages divide into
     while (h->box_rows < moe::kRowsKeyTile && config->page_size % (2 * h->box_rows) == 0) h->box_rows *= 2;
     h->box_tile = h->box_rows;
@@ -303,9 +316,7 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
       p += align256(b);
       return at;
     };
-    h->seq_of = reinterpret_cast<int32_t*>(carve(N * 4));
-    h->share = reinterpret_cast<long long*>(carve(2 * 8));
-    for (int i = 0; i < 2; ++i) h->own_off[i] = reinterpret_cast<int32_t*>(carve(S * 4));
+    for (int i = 0; i < 2; ++i) h->info[i] = reinterpret_cast<int2*>(carve(NR * 8));
     h->part_o = reinterpret_cast<float*>(carve(h->part_rows * h->DP * 4));
     h->part_ml = reinterpret_cast<float2*>(carve(h->part_rows * 8));
   }
@@ -446,10 +457,6 @@ moe_status_t moe_attn_forward(moe_attn_t* h, const void* q, int64_t q_stride, co
   if (b->prefix_len > 0 && !b->prefix_pages)
     return set_error(MOE_ERR_INVALID_ARG, "%s: prefix_pages must not be NULL", fn);
   if (b->causal != 0 && b->causal != 1) return set_error(MOE_ERR_INVALID_ARG, "%s: causal must be 0 or 1", fn);
-  // tiles of one key head, counted in 32 bits on the device
-  const long long blocks = ((long long)b->max_q_len * (c.num_q_heads / c.num_kv_heads) + 15) / 16;
-  if ((b->max_seq_len + moe::kRowsKeyTile - 1LL) / moe::kRowsKeyTile * blocks > (1LL << 30) / b->num_seqs)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs * max_q_len * max_seq_len is more than one call takes", fn);
   st = check_rows(h, fn, "q", q, q_stride, c.num_q_heads);
   if (st == MOE_OK) st = check_rows(h, fn, "out", out, out_stride, c.num_q_heads);
   if (st != MOE_OK) return st;
@@ -483,7 +490,6 @@ moe_status_t moe_attn_forward(moe_attn_t* h, const void* q, int64_t q_stride, co
   a.out_stride = out_stride;
   a.lse = lse;
   a.err = h->err;
-  a.seq_of = h->seq_of;
   return forward(h, a, static_cast<cudaStream_t>(stream));
 }
 

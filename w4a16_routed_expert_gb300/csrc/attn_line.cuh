@@ -6,52 +6,37 @@
 
 namespace moe {
 
-// Keys the row block starting at row r0 of a sequence's n * g rows reads: as
-// many as its last token sees.
+// Keys that row block rb of a sequence's n * g rows reads: as many as its
+// last token sees.
 __device__ __forceinline__ int block_keys(const AttnArgs& a, const LineArgs& ln, int keys, int n, int rb) {
   const int last = min(n * a.g, (rb + 1) * ln.row_block) - 1;
-  return keys_seen(a, keys, n, last / a.g);
+  return a.causal ? keys_seen(a, keys, n, last / a.g) : keys;
 }
-// Tiles of a sequence for one key head.
-__device__ __forceinline__ int seq_tiles(const AttnArgs& a, const LineArgs& ln, int keys, int n) {
-  const int blocks = (n * a.g + ln.row_block - 1) / ln.row_block;
-  int tiles = 0;
-  for (int rb = 0; rb < blocks; ++rb)
-    tiles += (block_keys(a, ln, keys, n, rb) + ln.key_tile - 1) / ln.key_tile;
-  return tiles;
-}
-// (key heads, row blocks, tiles each) of the prefix.
-__device__ __forceinline__ int prefix_blocks(const AttnArgs& a, const LineArgs& ln) {
-  return (int)(((long long)a.T * a.g + ln.row_block - 1) / ln.row_block);
-}
-__device__ __forceinline__ int prefix_tiles(const AttnArgs& a, const LineArgs& ln) {
-  return ln.has_prefix ? (a.prefix_len + ln.key_tile - 1) / ln.key_tile : 0;
-}
-__device__ __forceinline__ long long prefix_line(const AttnArgs& a, const LineArgs& ln) {
-  return (long long)a.Hk * prefix_blocks(a, ln) * prefix_tiles(a, ln);
+// Places on the line of a group that reads `keys` keys.
+__device__ __forceinline__ int group_span(const LineArgs& ln, int keys) {
+  return keys > 0 ? (keys + ln.key_tile - 1) / ln.key_tile + ln.weight : 0;
 }
 
-// Whole block (NT threads): own_off[b] = own tiles of one key head before
-// sequence b, in shared memory; returns their total. scratch: NT / 32 ints.
+// Whole block (NT threads): own_off[b] = places of one key head's groups
+// before sequence b, in shared memory; returns their total. scratch: NT / 32
+// ints.
 template <int NT>
 __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off, int32_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!ln.has_own) {
-    if (tid == 0) own_off[0] = 0;
-    __syncthreads();
-    return 0;
-  }
+  if (!ln.has_own) return 0;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int sum = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     int t0;
-    const int n = seq_tokens(a, b, &t0);
-    const int tiles = seq_tiles(a, ln, seq_keys(a, b), n);
-    own_off[b + 1] = tiles;
-    sum += tiles;
-    if (blockIdx.x == b % gridDim.x)
-      for (int i = 0; i < n; ++i) a.seq_of[t0 + i] = b;
+    const int n = seq_tokens(a, b, &t0), keys = seq_keys(a, b);
+    const int blocks = (n * a.g + ln.row_block - 1) / ln.row_block;
+    int span = 0;
+#pragma unroll 1
+    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, block_keys(a, ln, keys, n, rb));
+    own_off[b + 1] = span;
+    sum += span;
   }
   int incl = sum;
 #pragma unroll
@@ -68,6 +53,7 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
     total += scratch[w];
   }
   if (tid == 0) own_off[0] = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     base += own_off[b + 1];
     own_off[b + 1] = base;
@@ -76,95 +62,138 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
   return total;
 }
 
-// One block's part of one group.
+// One block's part of one group, handed through shared memory from the
+// copying warp to the others.
 struct Segment {
   int b;            // sequence, or -1: the prefix
   int h;            // key head
-  int tile, tiles;  // first tile of the group and number of tiles in this part
+  int tile, tiles;  // first tile of the group and number of tiles in this part (0: no more parts)
   int row0, rows;   // first row of the group among its sequence's (all tokens') rows, rows
   int t0, n;        // the sequence's (batch's) first token and tokens
   int klen;         // its keys
   int nkeys;        // keys the group reads (its last row's)
-  long long prow;   // first row of the partial
+  int prow;         // first row of the partial
+  int parts;        // the part with the group's first tile: parts of the group (else 0)
 };
+constexpr int kSegSlots = 4;  // parts handed ahead
 
-// The part of the line from tile x (x < end), this block's run.
-__device__ __forceinline__ Segment segment_at(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off,
-                                              long long x, long long end) {
-  Segment s;
-  const long long wp = prefix_line(a, ln);
-  int left;  // tiles of the group from s.tile on
-  long long base;
-  if (x < wp) {
-    const int nt = prefix_tiles(a, ln), nb = prefix_blocks(a, ln);
-    const int grp = (int)(x / nt);
-    s.b = -1;
-    s.tile = (int)(x - (long long)grp * nt);
-    left = nt - s.tile;
-    s.h = grp / nb;
-    const int rb = grp - s.h * nb;
-    s.t0 = 0;
-    s.n = a.T;
-    s.row0 = rb * ln.row_block;
-    s.rows = min(ln.row_block, a.T * a.g - s.row0);
-    s.klen = s.nkeys = a.prefix_len;
-    base = (long long)s.h * a.T * a.g + s.row0;
-  } else {
-    const long long y = x - wp;
-    int lo = 0, hi = a.B - 1;  // last b with own_off[b] * Hk <= y
+// The walk: every lane of a warp runs it with the same values.
+struct Walk {
+  int x, end, share;   // place, end of this block's run, places per block
+  int start, nt;       // the group's first place, its tiles
+  int blocks;          // row blocks of the sequence (the batch)
+  int rb;
+  Segment s;           // b, h, t0, n, klen, nkeys of the group
+
+  __device__ __forceinline__ void load_seq(const AttnArgs& a, const LineArgs& ln, int b) {
+    s.b = b;
+    s.n = seq_tokens(a, b, &s.t0);
+    s.klen = seq_keys(a, b);
+    blocks = (s.n * a.g + ln.row_block - 1) / ln.row_block;
+  }
+  __device__ __forceinline__ void set_group(const AttnArgs& a, const LineArgs& ln) {
+    s.nkeys = s.b < 0 ? s.klen : block_keys(a, ln, s.klen, s.n, rb);
+    nt = (s.nkeys + ln.key_tile - 1) / ln.key_tile;
+  }
+  // The first group of own keys that has any, from sequence b on.
+  __device__ __forceinline__ void first_own(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int b) {
+    while (b < a.B - 1 && own_off[b + 1] == own_off[b]) ++b;
+    load_seq(a, ln, b);
+    s.h = 0;
+    rb = 0;
+    set_group(a, ln);
+  }
+  // To the group after this one (its start is where this one ended); false
+  // after the last.
+  __device__ __forceinline__ bool next_group(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off) {
+    start += nt > 0 ? nt + ln.weight : 0;
+    if (++rb >= blocks) {
+      rb = 0;
+      if (++s.h >= a.Hk) {
+        if (!ln.has_own || s.b + 1 >= a.B) return false;
+        first_own(a, ln, own_off, s.b + 1);
+        return true;
+      }
+    }
+    set_group(a, ln);
+    return true;
+  }
+  // own_total: places of one key head's own groups (scan_own).
+  __device__ __forceinline__ void init(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int own_total) {
+    const int pblocks = ln.has_prefix ? (a.T * a.g + ln.row_block - 1) / ln.row_block : 0;
+    const int pspan = ln.has_prefix ? group_span(ln, a.prefix_len) : 0;
+    const int total_prefix = a.Hk * pblocks * pspan;
+    const int total = total_prefix + own_total * a.Hk;
+    share = max(1, (int)(((unsigned)total + ln.n_cta - 1) / (unsigned)ln.n_cta));
+    x = (int)min((long long)share * blockIdx.x, (long long)total);
+    end = (int)min((long long)x + share, (long long)total);
+    if (x >= end) return;
+    if (x < total_prefix) {
+      const int grp = x / pspan;
+      start = grp * pspan;
+      s.b = -1;
+      s.h = grp / pblocks;
+      rb = grp - s.h * pblocks;
+      blocks = pblocks;
+      s.t0 = 0;
+      s.n = a.T;
+      s.klen = a.prefix_len;
+      set_group(a, ln);
+      return;
+    }
+    const unsigned y = (unsigned)(x - total_prefix);
+    int lo = 0, hi = a.B - 1;  // last sequence that starts at or before y
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((long long)own_off[mid] * a.Hk <= y)
+      if ((unsigned)own_off[mid] * a.Hk <= y)
         lo = mid;
       else
         hi = mid - 1;
     }
-    s.b = lo;
-    const int per_head = own_off[lo + 1] - own_off[lo];
-    const long long r = y - (long long)own_off[lo] * a.Hk;
-    s.h = (int)(r / per_head);
-    int in = (int)(r - (long long)s.h * per_head);
-    s.n = seq_tokens(a, lo, &s.t0);
-    s.klen = seq_keys(a, lo);
-    const int blocks = (s.n * a.g + ln.row_block - 1) / ln.row_block;
-    int rb = 0;
-    left = 0;
-    for (; rb < blocks; ++rb) {
-      s.nkeys = block_keys(a, ln, s.klen, s.n, rb);
-      const int nt = (s.nkeys + ln.key_tile - 1) / ln.key_tile;
-      if (in < nt) {
-        left = nt - in;
-        break;
+    const int per_head = max(1, own_off[lo + 1] - own_off[lo]);
+    load_seq(a, ln, lo);
+    s.h = min((int)((y - (unsigned)own_off[lo] * a.Hk) / (unsigned)per_head), a.Hk - 1);
+    start = total_prefix + own_off[lo] * a.Hk + s.h * per_head;
+    rb = 0;
+    set_group(a, ln);
+    while (start + (nt > 0 ? nt + ln.weight : 0) <= x && rb + 1 < blocks) {
+      start += nt > 0 ? nt + ln.weight : 0;
+      ++rb;
+      set_group(a, ln);
+    }
+  }
+  // The next part of this block's run; false when there is none.
+  __device__ __forceinline__ bool next(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, Segment* out) {
+    while (x < end) {
+      const int first = start + ln.weight;  // the group's first tile
+      const int lo = max(x, first), hi = min(end, first + nt);
+      const bool some = hi > lo;
+      if (some) {
+        *out = s;
+        out->tile = lo - first;
+        out->tiles = hi - lo;
+        out->row0 = rb * ln.row_block;
+        out->rows = min(ln.row_block, s.n * a.g - out->row0);
+        out->prow = ln.part_row0 + (int)blockIdx.x * ln.part_rows + out->row0 + s.h * s.n * a.g +
+                    (s.b < 0 ? 0 : (ln.has_prefix * a.T + s.t0) * a.Hq);
+        out->parts = lo == first ? (first + nt - 1) / share - (int)blockIdx.x + 1 : 0;
       }
-      in -= nt;
+      // (lengths that change under the kernel move groups, but every step
+      // still goes on along the line or to a later group)
+      if (nt > 0) x = max(x + 1, first + nt);
+      if (x < end && !next_group(a, ln, own_off)) x = end;
+      if (some) return true;
     }
-    if (left == 0) {  // the lengths changed under the kernel: nothing to read, one tile on
-      record_error(a.err, kAttnErrBounds);
-      rb = in = s.nkeys = 0;
-      left = 1;
-    }
-    s.tile = in;
-    s.row0 = rb * ln.row_block;
-    s.rows = min(ln.row_block, s.n * a.g - s.row0);
-    base = ((long long)ln.has_prefix * a.T + s.t0) * a.g * a.Hk + (long long)s.h * s.n * a.g + s.row0;
+    return false;
   }
-  s.tiles = (int)min((long long)left, end - x);
-  s.prow = base + (long long)blockIdx.x * ln.part_rows;
-  return s;
-}
+};
 
-// Tile line of the launch: tiles per block, with the first block leaving what
-// the join needs in the workspace. All threads call it after scan_own.
-__device__ __forceinline__ long long line_share(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off,
-                                                int own_total, long long* total) {
-  *total = prefix_line(a, ln) + (long long)own_total * a.Hk;
-  const long long share = max(1LL, (*total + ln.n_cta - 1) / ln.n_cta);
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) *ln.share = share;
-    if (ln.has_own)
-      for (int b = threadIdx.x; b <= a.B; b += blockDim.x) ln.own_off[b] = own_off[b];
-  }
-  return share;
+// Leaves, for each row of a group, where its partials start and how many
+// there are (the part with the group's first tile does). r: row of the group.
+__device__ __forceinline__ void write_info(const AttnArgs& a, const LineArgs& ln, const Segment& s, int r) {
+  const int row = s.row0 + r, tok = row / a.g;
+  int2* info = s.b < 0 ? ln.info_prefix : ln.info_own;
+  info[(long long)(s.t0 + tok) * a.Hq + s.h * a.g + (row - tok * a.g)] = make_int2(s.prow + r, s.parts);
 }
 
 }  // namespace moe

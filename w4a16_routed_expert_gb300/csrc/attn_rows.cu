@@ -29,15 +29,16 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kMaxStages = 4;
 
 struct SmemPlan {
-  uint32_t q, merge, ml, bars, misc, off, bytes;
+  uint32_t q, merge, ml, bars, seg, misc, off, bytes;
 };
-__host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int stages, int B) {
+__host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int rows, int stages, int B) {
   SmemPlan p;
   p.q = (uint32_t)stages * 2 * kKT * DP * 2;
   p.merge = p.q + (uint32_t)MT * 16 * DP * 2;
-  p.ml = p.merge + 2u * MT * 16 * DP * 4;
+  p.ml = p.merge + 2u * MT * (rows > 8 ? 16 : 8) * DP * 4;
   p.bars = p.ml + (uint32_t)kWarps * MT * 16 * 8;
-  p.misc = p.bars + 2 * kMaxStages * 8;
+  p.seg = p.bars + 2 * (kMaxStages + kSegSlots) * 8;
+  p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 64;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
   return p;
@@ -51,9 +52,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const LineArgs ln, int stages, int box_log2, int late_wait) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const SmemPlan sp = smem_plan(DP, MT, stages, a.B);
+  const SmemPlan sp = smem_plan(DP, MT, ln.part_rows, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
+  uint64_t* seg_full = empty + kMaxStages;
+  uint64_t* seg_empty = seg_full + kSegSlots;
+  Segment* segs = reinterpret_cast<Segment*>(smem + sp.seg);
   volatile int* abort_flag = reinterpret_cast<int*>(smem + sp.misc);
   int32_t* scratch = reinterpret_cast<int32_t*>(smem + sp.misc) + 4;
   int32_t* own_off = reinterpret_cast<int32_t*>(smem + sp.off);
@@ -65,57 +69,75 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], kWarps);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   pdl_trigger();
   if (!late_wait) pdl_wait();
   const int own_total = scan_own<kThreads>(a, ln, own_off, scratch);
-  long long total;
-  const long long share = line_share(a, ln, own_off, own_total, &total);
-  const long long x0 = min(share * blockIdx.x, total), x1 = min(x0 + share, total);
+  if (!ln.has_own) __syncthreads();
   const int box = 1 << box_log2;
 
   if (warp == kWarps) {
-    // ------------------------------------------------------------- copies
+    // ---------------------------------------------- the walk and its copies
     // lane c < kKT / box copies the tile's box c of keys, lane 16 + c of values
     const int c = lane & 15;
     const bool mine = c < (kKT >> box_log2);
     const CUtensorMap* tm = lane < 16 ? &tk : &tv;
     const bool split = (a.D & 63) != 0;  // one box per 64 elements of the head
-    int st = 0;
-    uint32_t ph = 0;
+    int st = 0, slot_i = 0;
+    uint32_t ph = 0, sph = 0;
     int issued = 0;
     bool ok = true;
-    for (long long x = x0; x < x1 && ok;) {
-      const Segment s = segment_at(a, ln, own_off, x, x1);
+    Walk w;
+    w.init(a, ln, own_off, own_total);
+    while (ok) {
+      Segment s;
+      const bool some = w.next(a, ln, own_off, &s);
+      if (!some) s.tiles = 0;
+      ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
+      if (!ok) break;
+      if (lane == 0) {
+        segs[slot_i] = s;
+        mbar_arrive(&seg_full[slot_i]);
+      }
+      if (++slot_i == kSegSlots) {
+        slot_i = 0;
+        sph ^= 1u;
+      }
+      if (!some) break;
       const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      int slot = 0;  // of the page, of the lane's box of the current tile
       auto page_of = [&](int tile) {
         const int key = tile * kKT + (c << box_log2);
-        return mine && key < s.nkeys ? page_in_cache(a, __ldg(tab + key / a.page_size)) : -1;
+        if (!mine || key >= s.nkeys) return -1;
+        const int pg = key / a.page_size;
+        slot = key - pg * a.page_size;
+        return page_in_cache(a, __ldg(tab + pg));
       };
       int page = page_of(s.tile);
+#pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
-        const int tile = s.tile + i;
+        const int tile = s.tile + i, at = slot;
         const int next = i + 1 < s.tiles ? page_of(tile + 1) : -1;
         const int boxes = (min(kKT, max(0, s.nkeys - tile * kKT)) + box - 1) >> box_log2;
-        const bool got = mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * 2 * box * DP * 2);
         __syncwarp();
         if (page >= 0) {
           const uint32_t dst = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes + (lane < 16 ? 0u : kTileBytes) +
                                (uint32_t)c * box * DP * 2;
-          const int slot = (tile * kKT + (c << box_log2)) % a.page_size;
           if (split) {
 #pragma unroll
             for (int hf = 0; hf < NH; ++hf)
-              tma_load_5d(dst + (uint32_t)hf * box * 128, tm, hf * 64, slot, 0, s.h, page, &full[st]);
+              tma_load_5d(dst + (uint32_t)hf * box * 128, tm, hf * 64, at, 0, s.h, page, &full[st]);
           } else {
-            tma_load_5d(dst, tm, 0, slot, 0, s.h, page, &full[st]);
+            tma_load_5d(dst, tm, 0, at, 0, s.h, page, &full[st]);
           }
         }
         ++issued;
@@ -125,7 +147,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           ph ^= 1u;
         }
       }
-      x += s.tiles;
     }
     // a block that gave up lets its copies land before its memory is released
     if (!ok && lane == 0)
@@ -145,23 +166,46 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int qrow = (lane & 7) + (((lane >> 3) & 1) << 3), qsel = lane >> 4;
     float2* ml = reinterpret_cast<float2*>(smem + sp.ml);
     float* merge = reinterpret_cast<float*>(smem + sp.merge);
-    int st = 0;
-    uint32_t ph = 0;
+    int st = 0, slot_i = 0;
+    uint32_t ph = 0, sph = 0;
     bool ok = true;
-    for (long long x = x0; x < x1 && ok;) {
-      const Segment s = segment_at(a, ln, own_off, x, x1);
-      // queries: rows of 128-byte halves, swizzled as the boxes are; zeros
-      // beyond the group's rows and the head's elements
-      for (int i = tid; i < MT * 16 * DP / 8; i += kWarps * 32) {
-        const int r = i / (DP / 8), c8 = i % (DP / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
+    auto next_segment = [&](Segment* s) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], sph, abort_flag, a.err));
+      if (!got) return false;
+      *s = segs[slot_i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[slot_i]);
+      if (++slot_i == kSegSlots) {
+        slot_i = 0;
+        sph ^= 1u;
+      }
+      return s->tiles > 0;
+    };
+    // queries: rows of 128-byte halves, swizzled as the boxes are; zeros
+    // beyond the group's rows and the head's elements
+    constexpr int kQ = MT * 16 * DP / 8 / (kWarps * 32);  // 16-byte words of a thread
+    uint4 qv[kQ];
+    auto load_q = [&](const Segment& s) {
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
+        qv[i] = make_uint4(0, 0, 0, 0);
         if (r < s.rows && c8 * 8 < a.D) {
-          const int row = s.row0 + r, tok = s.t0 + row / a.g, hq = s.h * a.g + row % a.g;
-          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)tok * a.q_stride +
-                                              (long long)hq * a.D + c8 * 8);
+          const int row = s.row0 + r, tok = row / a.g, hq = s.h * a.g + row - tok * a.g;
+          qv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.t0 + tok) * a.q_stride +
+                                                  (long long)hq * a.D + c8 * 8);
         }
+      }
+    };
+    Segment s;
+    bool some = next_segment(&s);
+    if (some) load_q(s);
+    while (some) {
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
         *reinterpret_cast<uint4*>(smem + sp.q + (uint32_t)(c8 >> 3) * MT * 16 * 128 + (uint32_t)r * 128 +
-                                  (uint32_t)(((c8 & 7) ^ (r & 7)) << 4)) = v;
+                                  (uint32_t)(((c8 & 7) ^ (r & 7)) << 4)) = qv[i];
       }
       bar_compute();
       float o[MT][DP / 8][4];
@@ -184,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // keys that every row sees: no masking needed below it
       const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
 
+#pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
         const int k0 = (s.tile + i) * kKT + warp * 16;
         const bool got = mbar_wait(&full[st], ph, abort_flag, a.err);
@@ -300,6 +345,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (!ok) break;
+      // the next part's queries are on their way while this one is joined
+      const Segment cur = s;
+      some = next_segment(&s);
+      if (some) load_q(s);
 
       // ---- the four warps' results become one: a common maximum, then the
       // rescaled sums and output tiles added in a fixed order (3 into 1, 2
@@ -337,52 +386,57 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[m][n][2 * e + 1] *= f;
           }
         }
-      float4* buf = reinterpret_cast<float4*>(merge) + (warp & 1) * (MT * DP / 8 * 32) + lane;
-      if (warp >= 2) {
+      // [slot][row half of 8][tile, column block][lane]
+      const int halves = ln.part_rows > 8 ? 2 : 1;
+      float2* buf = reinterpret_cast<float2*>(merge) + (warp & 1) * (halves * MT * (DP / 8) * 32) + lane;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int e = 0; e < 2; ++e)
+        if (warp >= 2 && e < halves) {
 #pragma unroll
-          for (int n = 0; n < DP / 8; ++n)
-            buf[(m * (DP / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
-      }
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n)
+              buf[((e * MT + m) * (DP / 8) + n) * 32] = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
+        }
       bar_compute();
-      if (warp < 2) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int e = 0; e < 2; ++e)
+        if (warp < 2 && e < halves) {
 #pragma unroll
-          for (int n = 0; n < DP / 8; ++n) {
-            const float4 v = buf[(m * (DP / 8) + n) * 32];
-            o[m][n][0] += v.x;
-            o[m][n][1] += v.y;
-            o[m][n][2] += v.z;
-            o[m][n][3] += v.w;
-            if (warp == 1)
-              buf[(m * (DP / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
-          }
-      }
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) {
+              float2* at = buf + ((e * MT + m) * (DP / 8) + n) * 32;
+              const float2 v = *at;
+              o[m][n][2 * e] += v.x;
+              o[m][n][2 * e + 1] += v.y;
+              if (warp == 1) *at = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
+            }
+        }
       bar_compute();
       if (warp == 0) {
-        const float4* src = reinterpret_cast<const float4*>(merge) + MT * DP / 8 * 32 + lane;
+        const float2* src = reinterpret_cast<const float2*>(merge) + halves * MT * (DP / 8) * 32 + lane;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = m * 16 + g8 + 8 * e;
-            if (r < s.rows) {
-              float* dst = ln.part_o + (s.prow + r) * DP + t4 * 2;
+            if (r < cur.rows) {
+              float* dst = ln.part_o + (long long)(cur.prow + r) * DP + t4 * 2;
 #pragma unroll
               for (int n = 0; n < DP / 8; ++n) {
-                const float4 v = src[(m * (DP / 8) + n) * 32];
-                const float va = e ? v.z : v.x, vc = e ? v.w : v.y;
-                *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[m][n][2 * e] + va, o[m][n][2 * e + 1] + vc);
+                const float2 v = src[((e * MT + m) * (DP / 8) + n) * 32];
+                *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[m][n][2 * e] + v.x, o[m][n][2 * e + 1] + v.y);
               }
-              if (t4 == 0) ln.part_ml[s.prow + r] = make_float2(mt[m][e], lt[m][e]);
+              if (t4 == 0) {
+                ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
+                if (cur.parts) write_info(a, ln, cur, r);
+              }
             }
           }
       }
-      // the buffers are free again once the next group's queries are in
+      // the buffers are free again once the next part's queries are in
       // (its first barrier comes after warp 0's reads)
-      x += s.tiles;
     }
   }
   if (late_wait) pdl_wait();  // ends after the kernel before it, so what waits for this one waits for both
@@ -408,8 +462,8 @@ AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms) {
   // as many stages as let two blocks share an SM (228 KB, 1 KB of it kept per
   // block, and up to 1 KB to align the ring)
   for (p.stages = kMaxStages; p.stages > 2; --p.stages)
-    if (smem_plan(DP, MT, p.stages, B).bytes + 2048 <= 114 * 1024) break;
-  p.smem = smem_plan(DP, MT, p.stages, B).bytes + 1024;
+    if (smem_plan(DP, MT, rows, p.stages, B).bytes + 2048 <= 114 * 1024) break;
+  p.smem = smem_plan(DP, MT, rows, p.stages, B).bytes + 1024;
   p.n_cta = num_sms * (p.smem + 1024 <= 114 * 1024 ? 2 : 1);
   return p;
 }

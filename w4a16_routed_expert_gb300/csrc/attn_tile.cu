@@ -38,14 +38,14 @@ constexpr int kWarpCopy = 8, kWarpMma = 9;
 constexpr int kMaxStages = 8;
 
 struct SmemPlan {
-  uint32_t ring, bars, misc, off, bytes;
+  uint32_t ring, bars, seg, misc, off, bytes;
 };
 __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
   SmemPlan p;
   p.ring = 2u * 128 * DP * 2;  // after the queries
   p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
-  p.misc = p.bars + (2 * kMaxStages + 9) * 8;
-  p.misc = (p.misc + 15) & ~15u;
+  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 10) * 8;
+  p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 64;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
   return p;
@@ -54,7 +54,7 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
 struct Misc {
   uint32_t tmem;
   int abort_flag;
-  int issued;      // stages handed to TMA
+  int issued;  // stages handed to TMA
   int mma_issued;
   int32_t scratch[12];
 };
@@ -76,7 +76,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 2;          // [2] logits in tensor memory
   uint64_t* p_full = s_full + 2;          // [2] probabilities in tensor memory
   uint64_t* o_full = p_full + 2;          // [2] output complete
-  uint64_t* drain = o_full + 2;
+  uint64_t* seg_full = o_full + 2;
+  uint64_t* seg_empty = seg_full + kSegSlots;
+  uint64_t* drain = seg_empty + kSegSlots;
+  Segment* segs = reinterpret_cast<Segment*>(smem + sp.seg);
   Misc* misc = reinterpret_cast<Misc*>(smem + sp.misc);
   int32_t* own_off = reinterpret_cast<int32_t*>(smem + sp.off);
   volatile int* abort_flag = &misc->abort_flag;
@@ -92,6 +95,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
+    }
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 9);  // eight softmax warps, the MMA thread
     }
     mbar_init(drain, 1);
     misc->abort_flag = 0;
@@ -109,9 +116,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // may rely on everything before this launch
   pdl_trigger();
   const int own_total = scan_own<kThreads>(a, ln, own_off, misc->scratch);
-  long long total;
-  const long long share = line_share(a, ln, own_off, own_total, &total);
-  const long long x0 = min(share * blockIdx.x, total), x1 = min(x0 + share, total);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -122,42 +126,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kWarpCopy) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kWarpCopy) {
-    // --------------------------------------------------------------- copies
+    // ------------------------------------------------ the walk and its copies
     // lane (box, half of the head): one box of every key and value tile
     const int c = lane / NH, hf = lane % NH;
     const int box = 1 << box_log2;
     const bool mine = c < (kKT >> box_log2);
     const bool split = (a.D & 63) != 0;
     const int cx = split ? hf * 64 : 0, ch = split ? 0 : hf;
-    int st = 0, issued = 0;
-    uint32_t ph = 0;
+    const uint32_t dst0 = smem_u32(smem) + sp.ring + (uint32_t)hf * kHalf + (uint32_t)c * box * 128;
+    int st = 0, issued = 0, slot_i = 0;
+    uint32_t ph = 0, sph = 0;
     bool ok = true;
-    for (long long x = x0; x < x1 && ok;) {
-      const Segment s = segment_at(a, ln, own_off, x, x1);
+    Walk w;
+    w.init(a, ln, own_off, own_total);
+    while (ok) {
+      Segment s;
+      const bool some = w.next(a, ln, own_off, &s);
+      if (!some) s.tiles = 0;
+      ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
+      if (!ok) break;
+      if (lane == 0) {
+        segs[slot_i] = s;
+        mbar_arrive(&seg_full[slot_i]);
+      }
+      if (++slot_i == kSegSlots) {
+        slot_i = 0;
+        sph ^= 1u;
+      }
+      if (!some) break;
       const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      int slot = 0;  // of the page, of the lane's box of the current tile
       auto page_of = [&](int tile) {
         const int key = tile * kKT + (c << box_log2);
-        return mine && key < s.nkeys ? page_in_cache(a, __ldg(tab + key / a.page_size)) : -1;
+        if (!mine || key >= s.nkeys) return -1;
+        const int pg = key / a.page_size;
+        slot = key - pg * a.page_size;
+        return page_in_cache(a, __ldg(tab + pg));
       };
       int page = page_of(s.tile);
+#pragma unroll 1
       for (int i = 0; i < s.tiles && ok; ++i) {
-        const int tile = s.tile + i;
+        const int tile = s.tile + i, at = slot;
         const int next = i + 1 < s.tiles ? page_of(tile + 1) : -1;
         const int boxes = (min(kKT, max(0, s.nkeys - tile * kKT)) + box - 1) >> box_log2;
-        const int slot = (tile * kKT + (c << box_log2)) % a.page_size;
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          const bool got = mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
+          if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
           __syncwarp();
           if (page >= 0)
-            tma_load_5d(smem_u32(smem) + sp.ring + (uint32_t)st * kTileBytes + (uint32_t)hf * kHalf +
-                            (uint32_t)c * box * 128,
-                        kv ? &tv : &tk, cx, slot, ch, s.h, page, &full[st]);
+            tma_load_5d(dst0 + (uint32_t)st * kTileBytes, kv ? &tv : &tk, cx, at, ch, s.h, page, &full[st]);
           ++issued;
           if (++st == stages) {
             st = 0;
@@ -166,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         page = next;
       }
-      x += s.tiles;
     }
     if (lane == 0) misc->issued = issued;
   } else if (warp == kWarpMma) {
@@ -174,9 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t id_s = attn_idesc(128, kKT, kBf16, false);
       constexpr uint32_t id_o = attn_idesc(128, DP, kBf16, true);
-      const uint32_t ring = smem_u32(smem) + sp.ring;
-      int st = 0;
-      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+      // descriptors: addresses count 16 bytes in the low bits and stay inside
+      // them, so a tile's are its stage's plus a constant
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem));
+      const uint64_t dk = smem_desc_sw128(smem_u32(smem) + sp.ring);
+      const uint64_t dv = smem_desc_rows_k(smem_u32(smem) + sp.ring, kHalf);
+      int st = 0, slot_i = 0;
+      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, sph = 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.err); };
       auto step = [&]() {
         if (++st == stages) {
@@ -185,19 +207,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto qk = [&](int t, int stage) {
-        const uint32_t qa = smem_u32(smem) + (uint32_t)t * kTileBytes, kb = ring + (uint32_t)stage * kTileBytes;
+        const uint64_t q = dq + (uint64_t)(t * (kTileBytes >> 4)), k0 = dk + (uint64_t)(stage * (kTileBytes >> 4));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32;
-          mma_f16_ss(tmem + t * 128, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), id_s, k > 0);
+          const uint64_t off = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
+          mma_f16_ss(tmem + t * 128, q + off, k0 + off, id_s, k > 0);
         }
-        misc->mma_issued = 1;
         mma_commit(&s_full[t]);
       };
       bool ok = true;
-      for (long long x = x0; x < x1 && ok;) {
-        const Segment s = segment_at(a, ln, own_off, x, x1);
-        const int nt = s.rows > 128 ? 2 : 1;
+      while (ok) {
+        ok = wait(&seg_full[slot_i], sph);
+        if (!ok) break;
+        const int tiles = segs[slot_i].tiles, nt = segs[slot_i].rows > 128 ? 2 : 1;
+        mbar_arrive(&seg_empty[slot_i]);
+        if (++slot_i == kSegSlots) {
+          slot_i = 0;
+          sph ^= 1u;
+        }
+        if (tiles == 0) break;
+        misc->mma_issued = 1;
         ok = wait(&full[st], ph);
         for (int t = 0; t < nt && ok; ++t) {
           ok = wait(&q_full[t], qph[t]);
@@ -209,32 +238,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         mma_commit(&empty[st]);
         step();
-        for (int i = 0; i < s.tiles && ok; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < tiles && ok; ++i) {
           const int vst = st;
+          const bool more = i + 1 < tiles;
+          // the tile's values and the next one's keys, before the wait for
+          // probabilities: that one is on the critical path
           ok = wait(&full[st], ph);
-          if (!ok) break;
           step();
-          const bool more = i + 1 < s.tiles;
-          for (int t = 0; t < nt; ++t) {
+          if (ok && more) ok = wait(&full[st], ph);
+          const uint64_t v0 = dv + (uint64_t)(vst * (kTileBytes >> 4));
+#pragma unroll 1
+          for (int t = 0; t < nt && ok; ++t) {
             ok = wait(&p_full[t], pph[t]);
             pph[t] ^= 1u;
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = ring + (uint32_t)vst * kTileBytes;
 #pragma unroll
             for (int k = 0; k < kKT / 16; ++k)
-              mma_f16_ts(tmem + 256 + t * DP, tmem + t * 128 + k * 8, smem_desc_rows_k(vb + (uint32_t)k * 2048, kHalf),
-                         id_o, (i > 0 || k > 0) ? 1u : 0u);
-            if (!more) {
+              mma_f16_ts(tmem + 256 + t * DP, tmem + t * 128 + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o,
+                         (i > 0 || k > 0) ? 1u : 0u);
+            if (more)
+              qk(t, st);
+            else
               mma_commit(&o_full[t]);
-              continue;
-            }
-            if (t == 0) {
-              ok = wait(&full[st], ph);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            qk(t, st);
           }
           if (!ok) break;
           mma_commit(&empty[vst]);
@@ -243,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             step();
           }
         }
-        x += s.tiles;
       }
     }
     __syncwarp();
@@ -275,18 +301,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    uint32_t sph = 0, oph = 0;
-    long long idx = 0;  // ring position of the segment's first key tile
-    Segment s;
-    if (x0 < x1) {
-      s = segment_at(a, ln, own_off, x0, x1);
-      if (t == 0 || s.rows > 128) {
-        load_q(s);
-        arrive(&q_full[t]);
+    uint32_t sph = 0, oph = 0, gph = 0;
+    int slot_i = 0;
+    int vst = 0;  // ring stage of the next key tile, and its phase
+    uint32_t vph = 0;
+    auto next_segment = [&](Segment* s) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], gph, abort_flag, a.err));
+      if (!got) return false;
+      *s = segs[slot_i];
+      arrive(&seg_empty[slot_i]);
+      if (++slot_i == kSegSlots) {
+        slot_i = 0;
+        gph ^= 1u;
       }
+      return s->tiles > 0;
+    };
+    Segment s;
+    bool some = next_segment(&s), ok = true;
+    if (some && (t == 0 || s.rows > 128)) {
+      load_q(s);
+      arrive(&q_full[t]);
     }
-    bool ok = true;
-    for (long long x = x0; x < x1 && ok;) {
+    while (some) {
       const bool used = t == 0 || s.rows > 128;
       const bool any_row = t * 128 + (warp & 3) * 32 < s.rows;  // this warp has a row
       float mref = -INFINITY;
@@ -295,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = s.row0 + min(r, s.rows - 1);
         const int lim = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
         const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
+#pragma unroll 1
         for (int i = 0; i < s.tiles; ++i) {
           const int k0 = (s.tile + i) * kKT;
           const bool got = mbar_wait(&s_full[t], sph, abort_flag, a.err);
@@ -363,17 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s.nkeys - k0 < kKT) {
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN)
-            const long long at = idx + 2 * i + 1;
-            const int vst = (int)(at % stages);
-            const bool there = mbar_wait(&full[vst], (uint32_t)(at / stages) & 1u, abort_flag, a.err);
+            int z = 2 * i + 1 + vst;  // the tile's values' place in the ring
+            const uint32_t zph = vph ^ ((uint32_t)(z / stages) & 1u);
+            z %= stages;
+            const bool there = mbar_wait(&full[z], zph, abort_flag, a.err);
             if (!__all_sync(0xffffffffu, there)) {
               ok = false;
               break;
             }
             const int here = max(0, s.nkeys - k0);
-            unsigned char* vt = smem + sp.ring + (uint32_t)vst * kTileBytes;
-            for (int z = tid & 127; z < (kKT - here) * (DP / 8); z += 128) {
-              const int zr = here + z / (DP / 8), c8 = z % (DP / 8);
+            unsigned char* vt = smem + sp.ring + (uint32_t)z * kTileBytes;
+            for (int y = tid & 127; y < (kKT - here) * (DP / 8); y += 128) {
+              const int zr = here + y / (DP / 8), c8 = y % (DP / 8);
               *reinterpret_cast<uint4*>(vt + (uint32_t)(c8 >> 3) * kHalf + (uint32_t)zr * 128 +
                                         (uint32_t)((c8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
@@ -384,16 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      const Segment cur = s;
-      x += s.tiles;
-      idx += 2 * (long long)s.tiles;
-      bool next_used = false;
-      if (x < x1) {
-        // the last Q K^T of this part has completed: its queries' place is free
-        s = segment_at(a, ln, own_off, x, x1);
-        next_used = t == 0 || s.rows > 128;
-        if (next_used) load_q(s);
+      {
+        const int z = vst + 2 * s.tiles;
+        vph ^= (uint32_t)(z / stages) & 1u;
+        vst = z % stages;
       }
+      const Segment cur = s;
+      some = next_segment(&s);
+      const bool next_used = some && (t == 0 || s.rows > 128);
+      if (next_used) load_q(s);  // the last Q K^T of this part has completed: its queries' place is free
       if (used) {
         const bool got = mbar_wait(&o_full[t], oph, abort_flag, a.err);
         oph ^= 1u;
@@ -403,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any_row) {
-          float* dst = ln.part_o + (cur.prow + r) * DP;
+          float* dst = ln.part_o + (long long)(cur.prow + r) * DP;
 #pragma unroll
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
@@ -415,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(dst + c * 32 + e * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
-          if (r < cur.rows) ln.part_ml[cur.prow + r] = make_float2(mref, l2.x + l2.y);
+          if (r < cur.rows) {
+            ln.part_ml[cur.prow + r] = make_float2(mref, l2.x + l2.y);
+            if (cur.parts) write_info(a, ln, cur, r);
+          }
         }
         tc_fence_before();
       }
