@@ -16,13 +16,20 @@
 //                   tensor memory of its number mod 4); queries in, output out
 //   warp 8          TMA: pages to shared memory, 128-byte swizzle, keys and
 //                   values in turn through one ring
-//   warp 9          tensor memory and the single thread that issues the MMAs:
-//                   P V of a tile, then the next Q K^T of the same rows, so
-//                   that one row tile's products run under the other's softmax
+//   warp 9          tensor memory and the MMAs, issued by one elected lane:
+//                   P V of a key tile, then the next Q K^T of the same rows,
+//                   row tiles in turn, so that one's products run under the
+//                   other's softmax (with a warp for each row tile the two
+//                   fell into step, both in softmax, then both waiting for
+//                   products: 3900 cycles a key tile instead of 3000)
+//   warp 10         waits for the copies in the MMA warp's place and joins the
+//                   probabilities' barrier: a wait costs ~170 cycles even when
+//                   it is complete, and the tensor cores hold only a few MMAs
+//                   in advance, so the MMA warp waits once a row tile
 // Tensor memory: two S tiles (P takes the first half of S's columns) and two
 // output tiles, 512 columns at head size 128.
 //
-// MMAs of one thread run in order, so Q K^T of the next tile may overwrite
+// MMAs of one lane run in order, so Q K^T of the next tile may overwrite
 // the columns that the P V issued just before it reads; and a completed
 // Q K^T means the P V before it has completed, so the softmax warps may
 // rescale the output without another barrier.
@@ -33,8 +40,8 @@ namespace moe {
 namespace {
 
 constexpr int kKT = kTileKeyTile;
-constexpr int kThreads = 12 * 32;  // three warpgroups: two of softmax, one of copies and MMAs
-constexpr int kWarpCopy = 8, kWarpMma = 9;
+constexpr int kThreads = 11 * 32;
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLanded = 10;
 constexpr int kMaxStages = 8;
 
 struct SmemPlan {
@@ -46,7 +53,7 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
   p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
   p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 10) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
-  p.off = p.misc + 64;
+  p.off = p.misc + 80;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
   return p;
 }
@@ -58,6 +65,7 @@ struct Misc {
   int mma_issued;
   int32_t scratch[12];
 };
+static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -93,12 +101,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 4);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[t], 5);  // four softmax warps, kWarpLanded
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 9);  // eight softmax warps, the MMA thread
+      mbar_init(&seg_empty[i], 10);  // eight softmax warps, kWarpMma, kWarpLanded
     }
     mbar_init(drain, 1);
     misc->abort_flag = 0;
@@ -121,10 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc->tmem;
 
-  // registers: 168 a thread at launch; a softmax thread holds 128 logits, and
-  // 2 x 208 + 88 = 3 x 168
   if (warp >= kWarpCopy) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kWarpCopy) {
     // ------------------------------------------------ the walk and its copies
     // lane (box, half of the head): one box of every key and value tile
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) misc->issued = issued;
   } else if (warp == kWarpMma) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
+    {
       constexpr uint32_t id_s = attn_idesc(128, kKT, kBf16, false);
       constexpr uint32_t id_o = attn_idesc(128, DP, kBf16, true);
       // descriptors: addresses count 16 bytes in the low bits and stay inside
@@ -199,7 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv = smem_desc_rows_k(smem_u32(smem) + sp.ring, kHalf);
       int st = 0, slot_i = 0;
       uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, sph = 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.err); };
+      const uint32_t elect = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
+      };
       auto step = [&]() {
         if (++st == stages) {
           st = 0;
@@ -211,22 +220,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint64_t off = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
-          mma_f16_ss(tmem + t * 128, q + off, k0 + off, id_s, k > 0);
+          mma_ss(elect, tm + t * 128, q + off, k0 + off, id_s, k > 0);
         }
-        mma_commit(&s_full[t]);
+        commit_elect(elect, &s_full[t]);
       };
       bool ok = true;
       while (ok) {
         ok = wait(&seg_full[slot_i], sph);
         if (!ok) break;
-        const int tiles = segs[slot_i].tiles, nt = segs[slot_i].rows > 128 ? 2 : 1;
-        mbar_arrive(&seg_empty[slot_i]);
+        const int tiles = __shfl_sync(0xffffffffu, segs[slot_i].tiles, 0);
+        const int nt = __shfl_sync(0xffffffffu, segs[slot_i].rows, 0) > 128 ? 2 : 1;
+        __syncwarp();
+        if (elect) mbar_arrive(&seg_empty[slot_i]);
         if (++slot_i == kSegSlots) {
           slot_i = 0;
           sph ^= 1u;
         }
         if (tiles == 0) break;
-        misc->mma_issued = 1;
+        if (elect) misc->mma_issued = 1;
         ok = wait(&full[st], ph);
         for (int t = 0; t < nt && ok; ++t) {
           ok = wait(&q_full[t], qph[t]);
@@ -236,52 +247,86 @@ __global__ void __launch_bounds__(kThreads, 1)
           qk(t, st);
         }
         if (!ok) break;
-        mma_commit(&empty[st]);
+        commit_elect(elect, &empty[st]);
         step();
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
           const int vst = st;
           const bool more = i + 1 < tiles;
-          // the tile's values and the next one's keys, before the wait for
-          // probabilities: that one is on the critical path
-          ok = wait(&full[st], ph);
           step();
-          if (ok && more) ok = wait(&full[st], ph);
           const uint64_t v0 = dv + (uint64_t)(vst * (kTileBytes >> 4));
 #pragma unroll 1
-          for (int t = 0; t < nt && ok; ++t) {
+          for (int t = 0; t < nt; ++t) {
+            // probabilities in tensor memory, this tile's values and the next
+            // one's keys in shared memory
             ok = wait(&p_full[t], pph[t]);
             pph[t] ^= 1u;
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kKT / 16; ++k)
-              mma_f16_ts(tmem + 256 + t * DP, tmem + t * 128 + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o,
-                         (i > 0 || k > 0) ? 1u : 0u);
+              mma_ts(elect, tm + 256 + t * DP, tm + t * 128 + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o,
+                     (i > 0 || k > 0) ? 1u : 0u);
+            if (t == nt - 1) commit_elect(elect, &empty[vst]);
             if (more)
               qk(t, st);
             else
-              mma_commit(&o_full[t]);
+              commit_elect(elect, &o_full[t]);
           }
-          if (!ok) break;
-          mma_commit(&empty[vst]);
-          if (more) {
-            mma_commit(&empty[st]);
+          if (ok && more) {
+            commit_elect(elect, &empty[st]);
             step();
           }
         }
       }
     }
-    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- landed
+    int st = 0, slot_i = 0;
+    uint32_t ph = 0, sph = 0, pph[2] = {1, 1};  // p_full: parity of the phase before the one to join
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
+    };
+    auto landed = [&]() {
+      if (!wait(&full[st], ph)) return false;
+      if (++st == stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+      return true;
+    };
+    bool ok = true;
+    while (ok) {
+      ok = wait(&seg_full[slot_i], sph);
+      if (!ok) break;
+      const int tiles = segs[slot_i].tiles, nt = segs[slot_i].rows > 128 ? 2 : 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[slot_i]);
+      if (++slot_i == kSegSlots) {
+        slot_i = 0;
+        sph ^= 1u;
+      }
+      if (tiles == 0) break;
+      ok = landed();
+#pragma unroll 1
+      for (int i = 0; i < tiles && ok; ++i) {
+        ok = landed() && (i + 1 == tiles || landed());
+        for (int t = 0; t < nt && ok; ++t) {
+          ok = wait(&p_full[t], pph[t]);  // the phase before is over: this arrival counts for the next
+          pph[t] ^= 1u;
+          if (ok && lane == 0) mbar_arrive(&p_full[t]);
+        }
+      }
+    }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;                       // row tile
     const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the group
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * DP;
     const float sc = a.scale * 1.44269504088896340736f;
+    const float2 sc2 = make_float2(sc, sc);
     unsigned char* qtile = smem + (uint32_t)t * kTileBytes;
     const int rl = r & 127;
     auto load_q = [&](const Segment& s) {
@@ -342,59 +387,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (any_row) {
-            uint32_t sr[4][32];
+            const bool edge = k0 + kKT > all_see;
+            uint32_t p[64];
+            float2 lt;
+            // The weights are taken against the reference maximum as it stands
+            // while the tile's own maximum is still being found, so neither
+            // waits for the other; only when a row passes the reference by
+            // more than kLazy (always on the first tile) is it moved and the
+            // tile, still in tensor memory, done again.
+#pragma unroll 1
+            while (true) {
+              const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
+              const float2 nref = make_float2(-ref, -ref);
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              lt = make_float2(0.f, 0.f);
+              uint32_t sr[2][32];
+              tmem_ld32(ts, sr[0]);
+              tmem_ld_wait_for(sr[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, sr[c]);
-            tmem_ld_wait();
-            if (k0 + kKT > all_see) {
+              for (int c = 0; c < 4; ++c) {
+                uint32_t(&v)[32] = sr[c & 1];
+                if (c < 3) tmem_ld32(ts + (c + 1) * 32, sr[(c + 1) & 1]);
+                if (edge) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+                  for (int e = 0; e < 32; ++e)
+                    if (k0 + c * 32 + e >= lim) v[e] = 0xff800000u;
+                }
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (k0 + c * 32 + e >= lim) sr[c][e] = 0xff800000u;
-            }
-            float mx[4];
+                for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              mx[c] = __uint_as_float(sr[c][0]);
-#pragma unroll
-              for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][e]));
-            }
-            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-            if (__any_sync(0xffffffffu, m > mref + kLazy)) {
+                for (int e = 0; e < 16; ++e) {
+                  float2 w = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, nref);
+                  w.x = exp2_fast(w.x);
+                  w.y = exp2_fast(w.y);
+                  lt = fadd2(lt, w);
+                  p[c * 16 + e] = Half16<T>::pack(w.x, w.y);
+                }
+                if (c < 3) tmem_ld_wait_for(sr[(c + 1) & 1]);
+              }
+              const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+              if (!__any_sync(0xffffffffu, m > mref + kLazy)) break;
               const float mn = fmaxf(mref, m);
               const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
               mref = mn;
               l2.x *= f;
               l2.y *= f;
               if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
-                  uint32_t o[32];
-                  tmem_ld32(to + c * 32, o);
-                  tmem_ld_wait();
+                  tmem_ld32(to + c * 32, sr[0]);
+                  tmem_ld_wait_for(sr[0]);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st32(to + c * 32, o);
+                  for (int e = 0; e < 32; ++e) sr[0][e] = __float_as_uint(__uint_as_float(sr[0][e]) * f);
+                  tmem_st32(to + c * 32, sr[0]);
                 }
               }
             }
-            const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
-            const float2 sc2 = make_float2(sc, sc), nref = make_float2(-ref, -ref);
-#pragma unroll
-            for (int hs = 0; hs < 2; ++hs) {
-              uint32_t p[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int c = hs * 2 + (e >> 4), w = (e & 15) * 2;
-                float2 v = ffma2(make_float2(__uint_as_float(sr[c][w]), __uint_as_float(sr[c][w + 1])), sc2, nref);
-                v.x = exp2_fast(v.x);
-                v.y = exp2_fast(v.y);
-                l2 = fadd2(l2, v);
-                p[e] = Half16<T>::pack(v.x, v.y);
-              }
-              tmem_st32(ts + hs * 32, p);
-            }
+            l2 = fadd2(l2, lt);
+            tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+            tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
             tmem_st_wait();
           }
           if (s.nkeys - k0 < kKT) {
@@ -445,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(to + c * 32, o);
-            tmem_ld_wait();
+            tmem_ld_wait_for(o);
             if (r < cur.rows) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -473,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < stages && i < n; ++i)
         mbar_wait(&full[i], (uint32_t)((n - 1 - i) / stages) & 1u, nullptr, nullptr);
     }
-    if (warp == kWarpMma && lane == 0 && misc->mma_issued) {
-      mma_commit(drain);
+    if (warp == kWarpMma && misc->mma_issued) {
+      commit_elect(elect_one(), drain);  // the lane that issued the MMAs
       mbar_wait(drain, 0, nullptr, nullptr);
     }
   }
