@@ -60,7 +60,8 @@ struct AttnArgs {
 // `row_block` query rows reads (a row is a query token and one of the g query
 // heads of a key head) form a group of key tiles: per key head and row block
 // of all tokens the prefix's tiles, then per sequence, key head and row block
-// the own keys'. All groups stand in one line, each as its tiles after
+// the own keys'. (Where sequences have row blocks of their own anyway, the
+// prefix's tiles stand at the front of every sequence's groups instead.) All groups stand in one line, each as its tiles after
 // `weight` empty places (what starting on a group costs, in tiles), and each
 // of n_cta blocks takes an equal run of it, so the work is even whatever the
 // lengths. A block's run within one group gives one partial result (running
@@ -71,6 +72,7 @@ struct LineArgs {
   int key_tile;          // keys of a tile
   int weight;
   int has_prefix, has_own;
+  int joined;            // the prefix's tiles stand at the front of every own group (has_prefix is 0)
   int n_cta;
   int part_rows;         // rows a partial takes at most: min(row_block, most rows of a group)
   int part_row0;         // this kernel's first row of partials
@@ -86,7 +88,9 @@ inline long long line_part_rows(const LineArgs& ln, long long T, long long Hq) {
 inline long long line_places(const AttnArgs& a, const LineArgs& ln) {
   const long long rows = (long long)a.T * a.g, kt = ln.key_tile, rb = ln.row_block;
   const long long prefix = ln.has_prefix ? (rows + rb - 1) / rb * ((a.prefix_len + kt - 1) / kt + ln.weight) : 0;
-  const long long own = ln.has_own ? (rows / rb + a.B) * ((a.max_seq_len + kt - 1) / kt + ln.weight) : 0;
+  const long long own = ln.has_own ? (rows / rb + a.B) * ((a.max_seq_len + kt - 1) / kt + ln.weight +
+                                                                (ln.joined ? (a.prefix_len + kt - 1) / kt : 0))
+                                 : 0;
   return (prefix + own) * a.Hk;
 }
 
@@ -111,7 +115,7 @@ cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const
 // Many rows to a key: 128-row tcgen05 tiles, two to a block, one block per SM.
 constexpr int kTileRows = 256;
 constexpr int kTileKeyTile = 128;
-constexpr int kTileWeight = 2;   // LineArgs::weight
+constexpr int kTileWeight = 3;   // LineArgs::weight
 cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              int box_slots, bool bf16, cudaStream_t s, bool pdl);
 

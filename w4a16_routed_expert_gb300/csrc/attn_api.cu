@@ -190,6 +190,11 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   // kernel, of which a block takes two.
   const bool tile_own = own_rows > moe::kRowsMax, tile_prefix = prefix_rows > moe::kRowsMax || (tile_own && prefix_rows);
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
+  // Sequences of a row block and more on average: no block would serve two of
+  // them, so the prefix is read in one go with the own keys (one partial
+  // instead of two; four chunks of 770 tokens behind 8200 keys:
+  // 382 us so, 413 apart).
+  const bool joined = tile_own && tile_prefix && (long long)a.T * a.g >= (long long)a.B * moe::kTileRows;
   moe::JoinArgs j = {};
   j.a = a;
   j.DP = h->DP;
@@ -202,8 +207,9 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
     ln->row_block = row_block;
     ln->key_tile = key_tile;
     ln->weight = weight;
-    ln->has_prefix = prefix;
+    ln->has_prefix = prefix && !joined;
     ln->has_own = own;
+    ln->joined = joined;
     ln->n_cta = n_cta;
     ln->part_rows = std::min(std::max(prefix ? prefix_rows : 0, own ? own_rows : 0), row_block);
     ln->part_row0 = (int)used;
@@ -212,7 +218,7 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
     ln->info_prefix = h->info[0];
     ln->info_own = h->info[1];
     used += moe::line_part_rows(*ln, a.T, a.Hq);
-    if (prefix) j.prefix_step = ln->part_rows;
+    if (ln->has_prefix) j.prefix_step = ln->part_rows;
     if (own) j.own_step = ln->part_rows;
     return moe::line_places(a, *ln) <= INT_MAX;
   };

@@ -12,10 +12,13 @@ __device__ __forceinline__ int block_keys(const AttnArgs& a, const LineArgs& ln,
   const int last = min(n * a.g, (rb + 1) * ln.row_block) - 1;
   return a.causal ? keys_seen(a, keys, n, last / a.g) : keys;
 }
-// Places on the line of a group that reads `keys` keys.
-__device__ __forceinline__ int group_span(const LineArgs& ln, int keys) {
-  return keys > 0 ? (keys + ln.key_tile - 1) / ln.key_tile + ln.weight : 0;
+// Tiles of `keys` keys; tiles of the prefix at the front of each own group.
+__device__ __forceinline__ int tiles_of(const LineArgs& ln, int keys) { return (keys + ln.key_tile - 1) / ln.key_tile; }
+__device__ __forceinline__ int front_tiles(const AttnArgs& a, const LineArgs& ln) {
+  return ln.joined ? tiles_of(ln, a.prefix_len) : 0;
 }
+// Places on the line of a group of `tiles` tiles.
+__device__ __forceinline__ int group_span(const LineArgs& ln, int tiles) { return tiles > 0 ? tiles + ln.weight : 0; }
 
 // Whole block (NT threads): own_off[b] = places of one key head's groups
 // before sequence b, in shared memory; returns their total. scratch: NT / 32
@@ -27,6 +30,7 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int sum = 0;
+  const int front = front_tiles(a, ln);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     int t0;
@@ -34,7 +38,7 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
     const int blocks = (n * a.g + ln.row_block - 1) / ln.row_block;
     int span = 0;
 #pragma unroll 1
-    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, block_keys(a, ln, keys, n, rb));
+    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of(ln, block_keys(a, ln, keys, n, rb)));
     own_off[b + 1] = span;
     sum += span;
   }
@@ -71,7 +75,8 @@ struct Segment {
   int row0, rows;   // first row of the group among its sequence's (all tokens') rows, rows
   int t0, n;        // the sequence's (batch's) first token and tokens
   int klen;         // its keys
-  int nkeys;        // keys the group reads (its last row's)
+  int nkeys;        // keys the group reads (its last row's), those of the tiles before `front` aside
+  int front;        // tiles of the prefix at the front of a sequence's group (LineArgs::joined)
   int prow;         // first row of the partial
   int parts;        // the part with the group's first tile: parts of the group (else 0)
 };
@@ -93,7 +98,8 @@ struct Walk {
   }
   __device__ __forceinline__ void set_group(const AttnArgs& a, const LineArgs& ln) {
     s.nkeys = s.b < 0 ? s.klen : block_keys(a, ln, s.klen, s.n, rb);
-    nt = (s.nkeys + ln.key_tile - 1) / ln.key_tile;
+    s.front = s.b < 0 ? 0 : front_tiles(a, ln);
+    nt = s.front + tiles_of(ln, s.nkeys);
   }
   // The first group of own keys that has any, from sequence b on.
   __device__ __forceinline__ void first_own(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int b) {
@@ -106,7 +112,7 @@ struct Walk {
   // To the group after this one (its start is where this one ended); false
   // after the last.
   __device__ __forceinline__ bool next_group(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off) {
-    start += nt > 0 ? nt + ln.weight : 0;
+    start += group_span(ln, nt);
     if (++rb >= blocks) {
       rb = 0;
       if (++s.h >= a.Hk) {
@@ -121,7 +127,7 @@ struct Walk {
   // own_total: places of one key head's own groups (scan_own).
   __device__ __forceinline__ void init(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int own_total) {
     const int pblocks = ln.has_prefix ? (a.T * a.g + ln.row_block - 1) / ln.row_block : 0;
-    const int pspan = ln.has_prefix ? group_span(ln, a.prefix_len) : 0;
+    const int pspan = ln.has_prefix ? group_span(ln, tiles_of(ln, a.prefix_len)) : 0;
     const int total_prefix = a.Hk * pblocks * pspan;
     const int total = total_prefix + own_total * a.Hk;
     share = max(1, (int)(((unsigned)total + ln.n_cta - 1) / (unsigned)ln.n_cta));
@@ -156,8 +162,8 @@ struct Walk {
     start = total_prefix + own_off[lo] * a.Hk + s.h * per_head;
     rb = 0;
     set_group(a, ln);
-    while (start + (nt > 0 ? nt + ln.weight : 0) <= x && rb + 1 < blocks) {
-      start += nt > 0 ? nt + ln.weight : 0;
+    while (start + group_span(ln, nt) <= x && rb + 1 < blocks) {
+      start += group_span(ln, nt);
       ++rb;
       set_group(a, ln);
     }

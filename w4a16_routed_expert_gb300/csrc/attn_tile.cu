@@ -159,21 +159,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
       }
       if (!some) break;
-      const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      const int32_t* own = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
       int slot = 0;  // of the page, of the lane's box of the current tile
+      int here = 0;  // keys of the tile that exist
       auto page_of = [&](int tile) {
-        const int key = tile * kKT + (c << box_log2);
-        if (!mine || key >= s.nkeys) return -1;
+        const bool pre = tile < s.front;
+        const int k0 = (pre ? tile : tile - s.front) * kKT, key = k0 + (c << box_log2);
+        const int nk = pre ? a.prefix_len : s.nkeys;
+        here = min(kKT, max(0, nk - k0));
+        if (!mine || key >= nk) return -1;
         const int pg = key / a.page_size;
         slot = key - pg * a.page_size;
-        return page_in_cache(a, __ldg(tab + pg));
+        return page_in_cache(a, __ldg((pre ? a.prefix_pages : own) + pg));
       };
       int page = page_of(s.tile);
 #pragma unroll 1
       for (int i = 0; i < s.tiles && ok; ++i) {
-        const int tile = s.tile + i, at = slot;
-        const int next = i + 1 < s.tiles ? page_of(tile + 1) : -1;
-        const int boxes = (min(kKT, max(0, s.nkeys - tile * kKT)) + box - 1) >> box_log2;
+        const int at = slot, boxes = (here + box - 1) >> box_log2;
+        const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : -1;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else {
+  } else if (warp == kWarpLanded) {
     // -------------------------------------------------------------- landed
     int st = 0, slot_i = 0;
     uint32_t ph = 0, sph = 0, pph[2] = {1, 1};  // p_full: parity of the phase before the one to join
@@ -327,20 +330,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * DP;
     const float sc = a.scale * 1.44269504088896340736f;
     const float2 sc2 = make_float2(sc, sc);
-    unsigned char* qtile = smem + (uint32_t)t * kTileBytes;
-    const int rl = r & 127;
-    auto load_q = [&](const Segment& s) {
-      const bool valid = r < s.rows;
-      const int row = s.row0 + r, tok = s.t0 + row / a.g, hq = s.h * a.g + row % a.g;
-      const T* src = static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (long long)hq * a.D;
-#pragma unroll
-      for (int c8 = 0; c8 < DP / 8; ++c8) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (valid && c8 * 8 < a.D) v = *reinterpret_cast<const uint4*>(src + c8 * 8);
-        *reinterpret_cast<uint4*>(qtile + (uint32_t)(c8 >> 3) * kHalf + (uint32_t)rl * 128 +
-                                  (uint32_t)(((c8 & 7) ^ (rl & 7)) << 4)) = v;
+    // queries of this row tile, 16 bytes a thread, consecutive threads along a
+    // row: asynchronous copies, complete after cp_async_wait_all; zeros beyond
+    // the group's rows and the head's elements
+    auto load_q = [&](const Segment* s) {
+      constexpr int kStep = 128 / (DP / 8);  // rows the 128 threads cover
+      const int z = tid & 127, c8 = z & (DP / 8 - 1);
+      const int step_tok = kStep / a.g, step_head = kStep - step_tok * a.g;
+      int rl = z / (DP / 8);
+      const int row = s->row0 + t * 128 + rl, rows = s->rows - t * 128;
+      int tok = row / a.g, hd = row - tok * a.g;
+      const T* src = static_cast<const T*>(a.q) + (long long)(s->t0 + tok) * a.q_stride +
+                     (long long)(s->h * a.g + hd) * a.D + c8 * 8;
+      const uint32_t dst = smem_u32(smem) + (uint32_t)t * kTileBytes + (uint32_t)(c8 >> 3) * kHalf;
+#pragma unroll 4
+      for (int i = 0; i < DP / 8; ++i, rl += kStep) {
+        const bool valid = rl < rows && c8 * 8 < a.D;
+        cp_async16(dst + (uint32_t)rl * 128 + (uint32_t)(((c8 & 7) ^ (rl & 7)) << 4), valid ? (const void*)src : a.q,
+                   valid);
+        src += (long long)step_tok * a.q_stride + (long long)step_head * a.D;
+        hd += step_head;
+        if (hd >= a.g) {  // the next token's first heads
+          hd -= a.g;
+          src += a.q_stride - (long long)a.g * a.D;
+        }
       }
-      fence_async_smem();
     };
     auto arrive = [&](uint64_t* bar) {
       __syncwarp();
@@ -350,25 +364,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot_i = 0;
     int vst = 0;  // ring stage of the next key tile, and its phase
     uint32_t vph = 0;
-    auto next_segment = [&](Segment* s) {
+    // the next part, in its slot; taken over with take_segment
+    auto peek_segment = [&]() {
       const bool got = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], gph, abort_flag, a.err));
-      if (!got) return false;
+      return got && segs[slot_i].tiles > 0;
+    };
+    auto take_segment = [&](Segment* s) {
       *s = segs[slot_i];
       arrive(&seg_empty[slot_i]);
       if (++slot_i == kSegSlots) {
         slot_i = 0;
         gph ^= 1u;
       }
-      return s->tiles > 0;
+    };
+    auto uses = [&](const Segment* s) { return t == 0 || s->rows > 128; };
+    auto q_arrive = [&]() {
+      cp_async_wait_all();
+      fence_async_smem();
+      arrive(&q_full[t]);
     };
     Segment s;
-    bool some = next_segment(&s), ok = true;
-    if (some && (t == 0 || s.rows > 128)) {
-      load_q(s);
-      arrive(&q_full[t]);
+    bool ok = true, some = peek_segment();
+    if (some) {
+      if (uses(&segs[slot_i])) {
+        load_q(&segs[slot_i]);
+        q_arrive();
+      }
+      take_segment(&s);
     }
     while (some) {
-      const bool used = t == 0 || s.rows > 128;
+      const bool used = uses(&s);
+      bool more = false, more_used = false;  // there is another part, and this row tile has rows in it
       const bool any_row = t * 128 + (warp & 3) * 32 < s.rows;  // this warp has a row
       float mref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
@@ -378,7 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
 #pragma unroll 1
         for (int i = 0; i < s.tiles; ++i) {
-          const int k0 = (s.tile + i) * kKT;
+          const bool pre = s.tile + i < s.front;  // a tile of the prefix before own keys
+          const int k0 = (s.tile + i - (pre ? 0 : s.front)) * kKT;
+          const int nk = pre ? a.prefix_len : s.nkeys;
           const bool got = mbar_wait(&s_full[t], sph, abort_flag, a.err);
           sph ^= 1u;
           if (!__all_sync(0xffffffffu, got)) {
@@ -386,17 +414,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
+          if (i + 1 == s.tiles) {
+            // this part's last Q K^T has completed: the next one's queries may
+            // come in under its softmax
+            more = peek_segment();
+            more_used = more && uses(&segs[slot_i]);
+            if (more_used) load_q(&segs[slot_i]);
+          }
           if (any_row) {
-            const bool edge = k0 + kKT > all_see;
+            const bool edge = k0 + kKT > (pre ? a.prefix_len : all_see);
+            const int seen = pre ? a.prefix_len : lim;
             uint32_t p[64];
             float2 lt;
             // The weights are taken against the reference maximum as it stands
             // while the tile's own maximum is still being found, so neither
             // waits for the other; only when a row passes the reference by
-            // more than kLazy (always on the first tile) is it moved and the
-            // tile, still in tensor memory, done again.
+            // more than kLazy is it moved and the tile, still in tensor
+            // memory, done again. The first tile sets it beforehand.
+            auto mask = [&](uint32_t(&v)[32], int c) {
+              if (edge) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (k0 + c * 32 + e >= seen) v[e] = 0xff800000u;
+              }
+            };
+            float m = -INFINITY;
+            bool move = i == 0;
+            if (move) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(ts + c * 32, v);
+                tmem_ld_wait_for(v);
+                mask(v, c);
+                float mx[2] = {m, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 32; ++e) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(v[e]));
+                m = fmaxf(mx[0], mx[1]);
+              }
+              m *= sc;
+            }
 #pragma unroll 1
             while (true) {
+              if (move) {
+                const float mn = fmaxf(mref, m);
+                const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
+                mref = mn;
+                l2.x *= f;
+                l2.y *= f;
+                if (i > 0) {
+#pragma unroll 1
+                  for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(to + c * 32, v);
+                    tmem_ld_wait_for(v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                    tmem_st32(to + c * 32, v);
+                  }
+                }
+              }
               const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
               const float2 nref = make_float2(-ref, -ref);
               float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -408,11 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 4; ++c) {
                 uint32_t(&v)[32] = sr[c & 1];
                 if (c < 3) tmem_ld32(ts + (c + 1) * 32, sr[(c + 1) & 1]);
-                if (edge) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (k0 + c * 32 + e >= lim) v[e] = 0xff800000u;
-                }
+                mask(v, c);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
 #pragma unroll
@@ -425,30 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (c < 3) tmem_ld_wait_for(sr[(c + 1) & 1]);
               }
-              const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-              if (!__any_sync(0xffffffffu, m > mref + kLazy)) break;
-              const float mn = fmaxf(mref, m);
-              const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
-              mref = mn;
-              l2.x *= f;
-              l2.y *= f;
-              if (i > 0) {
-#pragma unroll 1
-                for (int c = 0; c < DP / 32; ++c) {
-                  tmem_ld32(to + c * 32, sr[0]);
-                  tmem_ld_wait_for(sr[0]);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) sr[0][e] = __float_as_uint(__uint_as_float(sr[0][e]) * f);
-                  tmem_st32(to + c * 32, sr[0]);
-                }
-              }
+              m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+              move = __any_sync(0xffffffffu, m > mref + kLazy);
+              if (!move) break;
             }
             l2 = fadd2(l2, lt);
             tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
             tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
             tmem_st_wait();
           }
-          if (s.nkeys - k0 < kKT) {
+          if (nk - k0 < kKT) {
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN)
             int z = 2 * i + 1 + vst;  // the tile's values' place in the ring
@@ -459,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            const int here = max(0, s.nkeys - k0);
+            const int here = max(0, nk - k0);
             unsigned char* vt = smem + sp.ring + (uint32_t)z * kTileBytes;
             for (int y = tid & 127; y < (kKT - here) * (DP / 8); y += 128) {
               const int zr = here + y / (DP / 8), c8 = y % (DP / 8);
@@ -478,10 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         vph ^= (uint32_t)(z / stages) & 1u;
         vst = z % stages;
       }
-      const Segment cur = s;
-      some = next_segment(&s);
-      const bool next_used = some && (t == 0 || s.rows > 128);
-      if (next_used) load_q(s);  // the last Q K^T of this part has completed: its queries' place is free
+      if (!used) {
+        more = peek_segment();
+        more_used = more && uses(&segs[slot_i]);
+        if (more_used) load_q(&segs[slot_i]);
+      }
       if (used) {
         const bool got = mbar_wait(&o_full[t], oph, abort_flag, a.err);
         oph ^= 1u;
@@ -491,27 +551,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any_row) {
-          float* dst = ln.part_o + (long long)(cur.prow + r) * DP;
+          float* dst = ln.part_o + (long long)(s.prow + r) * DP;
 #pragma unroll
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(to + c * 32, o);
             tmem_ld_wait_for(o);
-            if (r < cur.rows) {
+            if (r < s.rows) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(dst + c * 32 + e * 4) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
             }
           }
-          if (r < cur.rows) {
-            ln.part_ml[cur.prow + r] = make_float2(mref, l2.x + l2.y);
-            if (cur.parts) write_info(a, ln, cur, r);
+          if (r < s.rows) {
+            ln.part_ml[s.prow + r] = make_float2(mref, l2.x + l2.y);
+            if (s.parts) write_info(a, ln, s, r);
           }
         }
         tc_fence_before();
       }
-      if (next_used) arrive(&q_full[t]);
+      if (more_used) q_arrive();
+      some = more;
+      if (some) take_segment(&s);
     }
+    cp_async_wait_all();  // (none are left unless a wait gave up)
   }
 
   // ------------------------------------------------------------- teardown
