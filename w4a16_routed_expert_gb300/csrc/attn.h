@@ -79,6 +79,7 @@ struct LineArgs {
   float* part_o;         // [rows][DP]: block c's partial of a group stands at the group's first row + c * part_rows
   float2* part_ml;       // [rows] maximum (log2 units), sum
   int2 *info_prefix, *info_own;  // [T][Hq] first partial row and number of partials, 0 between forwards
+  int final_prefix, final_own;   // 1: these groups' rows have no other partials, one part alone is the result
 };
 // Rows of partial results one kernel can write.
 inline long long line_part_rows(const LineArgs& ln, long long T, long long Hq) {

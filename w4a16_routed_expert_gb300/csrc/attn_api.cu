@@ -217,6 +217,8 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
     ln->part_ml = h->part_ml;
     ln->info_prefix = h->info[0];
     ln->info_own = h->info[1];
+    ln->final_own = joined || !prefix_rows;
+    ln->final_prefix = !own_rows;
     used += moe::line_part_rows(*ln, a.T, a.Hq);
     if (ln->has_prefix) j.prefix_step = ln->part_rows;
     if (own) j.own_step = ln->part_rows;

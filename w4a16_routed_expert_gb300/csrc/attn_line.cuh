@@ -6,16 +6,30 @@
 
 namespace moe {
 
+// KT keys of a tile, RB rows of a group at most: LineArgs' key_tile and
+// row_block as the kernel was built for (powers of two, so that no division
+// stands before its first copy).
+
 // Keys that row block rb of a sequence's n * g rows reads: as many as its
 // last token sees.
-__device__ __forceinline__ int block_keys(const AttnArgs& a, const LineArgs& ln, int keys, int n, int rb) {
-  const int last = min(n * a.g, (rb + 1) * ln.row_block) - 1;
+template <int RB>
+__device__ __forceinline__ int block_keys(const AttnArgs& a, int keys, int n, int rb) {
+  const int last = min(n * a.g, (rb + 1) * RB) - 1;
   return a.causal ? keys_seen(a, keys, n, last / a.g) : keys;
 }
 // Tiles of `keys` keys; tiles of the prefix at the front of each own group.
-__device__ __forceinline__ int tiles_of(const LineArgs& ln, int keys) { return (keys + ln.key_tile - 1) / ln.key_tile; }
+template <int KT>
+__device__ __forceinline__ int tiles_of(int keys) {
+  return (int)((unsigned)(keys + KT - 1) / KT);
+}
+template <int KT>
 __device__ __forceinline__ int front_tiles(const AttnArgs& a, const LineArgs& ln) {
-  return ln.joined ? tiles_of(ln, a.prefix_len) : 0;
+  return ln.joined ? tiles_of<KT>(a.prefix_len) : 0;
+}
+// Row blocks of n query tokens.
+template <int RB>
+__device__ __forceinline__ int row_blocks(const AttnArgs& a, int n) {
+  return (int)((unsigned)(n * a.g + RB - 1) / RB);
 }
 // Places on the line of a group of `tiles` tiles.
 __device__ __forceinline__ int group_span(const LineArgs& ln, int tiles) { return tiles > 0 ? tiles + ln.weight : 0; }
@@ -23,22 +37,22 @@ __device__ __forceinline__ int group_span(const LineArgs& ln, int tiles) { retur
 // Whole block (NT threads): own_off[b] = places of one key head's groups
 // before sequence b, in shared memory; returns their total. scratch: NT / 32
 // ints.
-template <int NT>
+template <int NT, int KT, int RB>
 __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off, int32_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!ln.has_own) return 0;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int sum = 0;
-  const int front = front_tiles(a, ln);
+  const int front = front_tiles<KT>(a, ln);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     int t0;
     const int n = seq_tokens(a, b, &t0), keys = seq_keys(a, b);
-    const int blocks = (n * a.g + ln.row_block - 1) / ln.row_block;
+    const int blocks = row_blocks<RB>(a, n);
     int span = 0;
 #pragma unroll 1
-    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of(ln, block_keys(a, ln, keys, n, rb)));
+    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of<KT>(block_keys<RB>(a, keys, n, rb)));
     own_off[b + 1] = span;
     sum += span;
   }
@@ -83,6 +97,7 @@ struct Segment {
 constexpr int kSegSlots = 4;  // parts handed ahead
 
 // The walk: every lane of a warp runs it with the same values.
+template <int KT, int RB>
 struct Walk {
   int x, end, share;   // place, end of this block's run, places per block
   int start, nt;       // the group's first place, its tiles
@@ -90,21 +105,21 @@ struct Walk {
   int rb;
   Segment s;           // b, h, t0, n, klen, nkeys of the group
 
-  __device__ __forceinline__ void load_seq(const AttnArgs& a, const LineArgs& ln, int b) {
+  __device__ __forceinline__ void load_seq(const AttnArgs& a, int b) {
     s.b = b;
     s.n = seq_tokens(a, b, &s.t0);
     s.klen = seq_keys(a, b);
-    blocks = (s.n * a.g + ln.row_block - 1) / ln.row_block;
+    blocks = row_blocks<RB>(a, s.n);
   }
   __device__ __forceinline__ void set_group(const AttnArgs& a, const LineArgs& ln) {
-    s.nkeys = s.b < 0 ? s.klen : block_keys(a, ln, s.klen, s.n, rb);
-    s.front = s.b < 0 ? 0 : front_tiles(a, ln);
-    nt = s.front + tiles_of(ln, s.nkeys);
+    s.nkeys = s.b < 0 ? s.klen : block_keys<RB>(a, s.klen, s.n, rb);
+    s.front = s.b < 0 ? 0 : front_tiles<KT>(a, ln);
+    nt = s.front + tiles_of<KT>(s.nkeys);
   }
   // The first group of own keys that has any, from sequence b on.
   __device__ __forceinline__ void first_own(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int b) {
     while (b < a.B - 1 && own_off[b + 1] == own_off[b]) ++b;
-    load_seq(a, ln, b);
+    load_seq(a, b);
     s.h = 0;
     rb = 0;
     set_group(a, ln);
@@ -126,8 +141,8 @@ struct Walk {
   }
   // own_total: places of one key head's own groups (scan_own).
   __device__ __forceinline__ void init(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int own_total) {
-    const int pblocks = ln.has_prefix ? (a.T * a.g + ln.row_block - 1) / ln.row_block : 0;
-    const int pspan = ln.has_prefix ? group_span(ln, tiles_of(ln, a.prefix_len)) : 0;
+    const int pblocks = ln.has_prefix ? row_blocks<RB>(a, a.T) : 0;
+    const int pspan = ln.has_prefix ? group_span(ln, tiles_of<KT>(a.prefix_len)) : 0;
     const int total_prefix = a.Hk * pblocks * pspan;
     const int total = total_prefix + own_total * a.Hk;
     share = max(1, (int)(((unsigned)total + ln.n_cta - 1) / (unsigned)ln.n_cta));
@@ -157,7 +172,7 @@ struct Walk {
         hi = mid - 1;
     }
     const int per_head = max(1, own_off[lo + 1] - own_off[lo]);
-    load_seq(a, ln, lo);
+    load_seq(a, lo);
     s.h = min((int)((y - (unsigned)own_off[lo] * a.Hk) / (unsigned)per_head), a.Hk - 1);
     start = total_prefix + own_off[lo] * a.Hk + s.h * per_head;
     rb = 0;
@@ -178,8 +193,8 @@ struct Walk {
         *out = s;
         out->tile = lo - first;
         out->tiles = hi - lo;
-        out->row0 = rb * ln.row_block;
-        out->rows = min(ln.row_block, s.n * a.g - out->row0);
+        out->row0 = rb * RB;
+        out->rows = min(RB, s.n * a.g - out->row0);
         out->prow = ln.part_row0 + (int)blockIdx.x * ln.part_rows + out->row0 + s.h * s.n * a.g +
                     (s.b < 0 ? 0 : (ln.has_prefix * a.T + s.t0) * a.Hq);
         out->parts = lo == first ? (first + nt - 1) / share - (int)blockIdx.x + 1 : 0;
@@ -194,12 +209,21 @@ struct Walk {
   }
 };
 
-// Leaves, for each row of a group, where its partials start and how many
-// there are (the part with the group's first tile does). r: row of the group.
-__device__ __forceinline__ void write_info(const AttnArgs& a, const LineArgs& ln, const Segment& s, int r) {
+// Whether the part is its rows' whole result, to be stored as it is.
+__device__ __forceinline__ bool whole(const LineArgs& ln, const Segment& s) {
+  return s.parts == 1 && (s.b < 0 ? ln.final_prefix : ln.final_own);
+}
+// The token and query head of row r of a group.
+__device__ __forceinline__ int2 row_place(const AttnArgs& a, const Segment& s, int r) {
   const int row = s.row0 + r, tok = row / a.g;
+  return make_int2(s.t0 + tok, s.h * a.g + row - tok * a.g);
+}
+// Leaves, for each row of a group, where its partials start and how many
+// there are (the part with the group's first tile does), or -1 where the
+// result is stored already.
+__device__ __forceinline__ void write_info(const AttnArgs& a, const LineArgs& ln, const Segment& s, int r, int2 at) {
   int2* info = s.b < 0 ? ln.info_prefix : ln.info_own;
-  info[(long long)(s.t0 + tok) * a.Hq + s.h * a.g + (row - tok * a.g)] = make_int2(s.prow + r, s.parts);
+  info[(long long)at.x * a.Hq + at.y] = whole(ln, s) ? make_int2(0, -1) : make_int2(s.prow + r, s.parts);
 }
 
 }  // namespace moe

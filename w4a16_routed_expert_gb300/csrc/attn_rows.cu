@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   pdl_trigger();
   if (!late_wait) pdl_wait();
-  const int own_total = scan_own<kThreads>(a, ln, own_off, scratch);
+  const int own_total = scan_own<kThreads, kKT, MT * 16>(a, ln, own_off, scratch);
   if (!ln.has_own) __syncthreads();
   const int box = 1 << box_log2;
 
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t ph = 0, sph = 0;
     int issued = 0;
     bool ok = true;
-    Walk w;
+    Walk<kKT, MT * 16> w;
     w.init(a, ln, own_off, own_total);
     while (ok) {
       Segment s;
@@ -422,15 +422,26 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 2; ++e) {
             const int r = m * 16 + g8 + 8 * e;
             if (r < cur.rows) {
+              const bool done = whole(ln, cur);
+              const int2 at = cur.parts ? row_place(a, cur, r) : make_int2(0, 0);
+              const float inv = inverse_sum(lt[m][e]);
               float* dst = ln.part_o + (long long)(cur.prow + r) * DP + t4 * 2;
+              T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D + t4 * 2;
 #pragma unroll
               for (int n = 0; n < DP / 8; ++n) {
                 const float2 v = src[((e * MT + m) * (DP / 8) + n) * 32];
-                *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[m][n][2 * e] + v.x, o[m][n][2 * e + 1] + v.y);
+                const float2 w = make_float2(o[m][n][2 * e] + v.x, o[m][n][2 * e + 1] + v.y);
+                if (!done)
+                  *reinterpret_cast<float2*>(dst + n * 8) = w;
+                else if (n * 8 < a.D)
+                  *reinterpret_cast<uint32_t*>(out + n * 8) = Half16<T>::pack(w.x * inv, w.y * inv);
               }
               if (t4 == 0) {
-                ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
-                if (cur.parts) write_info(a, ln, cur, r);
+                if (!done)
+                  ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
+                else if (a.lse)
+                  a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mt[m][e], lt[m][e]);
+                if (cur.parts) write_info(a, ln, cur, r, at);
               }
             }
           }

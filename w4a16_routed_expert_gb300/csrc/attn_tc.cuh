@@ -168,5 +168,13 @@ struct ProbBias<__half> {
 // only when a logit passes it by more than this many powers of two; any
 // reference gives the same quotient.
 constexpr float kLazy = 8.f;
+// 1 / sum (0 for a row that sees no key) and the natural logarithm of the sum
+// of exponentials, from the reference maximum (powers of two) and the sum
+// taken against it.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+template <typename T>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : 0.693147180559945309f * (m - ProbBias<T>::value + log2f(l));
+}
 
 }  // namespace moe

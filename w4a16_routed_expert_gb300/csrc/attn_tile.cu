@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // only now: a kernel that starts on this trigger and does not wait itself
   // may rely on everything before this launch
   pdl_trigger();
-  const int own_total = scan_own<kThreads>(a, ln, own_off, misc->scratch);
+  const int own_total = scan_own<kThreads, kKT, kTileRows>(a, ln, own_off, misc->scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int st = 0, issued = 0, slot_i = 0;
     uint32_t ph = 0, sph = 0;
     bool ok = true;
-    Walk w;
+    Walk<kKT, kTileRows> w;
     w.init(a, ln, own_off, own_total);
     while (ok) {
       Segment s;
@@ -551,20 +551,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any_row) {
+          const bool done = whole(ln, s);
+          const int2 at = s.parts ? row_place(a, s, r) : make_int2(0, 0);
+          const float l = l2.x + l2.y, inv = inverse_sum(l);
           float* dst = ln.part_o + (long long)(s.prow + r) * DP;
-#pragma unroll
+          T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D;
+#pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(to + c * 32, o);
             tmem_ld_wait_for(o);
             if (r < s.rows) {
+              if (!done) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
+                for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 v;
+                  v.x = Half16<T>::pack(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                  v.y = Half16<T>::pack(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                  v.z = Half16<T>::pack(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                  v.w = Half16<T>::pack(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                  if (c * 32 + e * 8 < a.D) *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = v;
+                }
+              }
             }
           }
           if (r < s.rows) {
-            ln.part_ml[s.prow + r] = make_float2(mref, l2.x + l2.y);
-            if (s.parts) write_info(a, ln, s, r);
+            if (!done)
+              ln.part_ml[s.prow + r] = make_float2(mref, l);
+            else if (a.lse)
+              a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l);
+            if (s.parts) write_info(a, ln, s, r, at);
           }
         }
         tc_fence_before();
