@@ -86,8 +86,8 @@ typedef struct {
 typedef struct {
   void* k_cache;       /* device, 16-byte aligned; both NULL: a handle for moe_attn_rotate only */
   void* v_cache;
-  const float* q_norm; /* device FP32 [D] weights of the query heads' norm, or NULL: no norm */
-  const float* k_norm; /* device FP32 [D] weights of the key heads' norm, or NULL: no norm */
+  const float* q_norm; /* device FP32 [D] weights of the query heads' norm, 16-byte aligned, or NULL: no norm */
+  const float* k_norm; /* the same of the key heads' norm */
 } moe_attn_buffers_t;
 
 typedef struct moe_attn moe_attn_t;

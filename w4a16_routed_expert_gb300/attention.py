@@ -16,6 +16,12 @@ import torch
 from . import capi
 from .layer import _ptr, _stream_handle
 
+try:  # the handle of a device's current stream without building a Stream object (3 us a call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
 _DTYPES = {torch.float16: capi.MOE_DTYPE_F16, torch.bfloat16: capi.MOE_DTYPE_BF16}
 _SCALINGS = {"none": capi.MOE_ROPE_NONE, "linear": capi.MOE_ROPE_LINEAR, "ntk": capi.MOE_ROPE_NTK,
              "yarn": capi.MOE_ROPE_YARN}
@@ -93,11 +99,20 @@ class PagedAttention:
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         return t.data_ptr(), st if T > 1 else heads * self.head_dim
 
+    def _new_rows(self, like, T, heads):
+        """A new [T][heads][head_dim] tensor, its pointer and token stride."""
+        t = torch.empty((T, heads, self.head_dim), dtype=self.dtype, device=like.device)
+        return t, t.data_ptr(), heads * self.head_dim
+
     @staticmethod
     def _ints(name, t, n):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
             raise ValueError(f"{name}: contiguous cuda int32 with at least {n} elements")
         return t.data_ptr()
+
+    @staticmethod
+    def _stream(stream, t):
+        return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
 
     def rotate(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor,
                q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
@@ -110,15 +125,17 @@ class PagedAttention:
         if q is not None:
             qp, qs = self._rows("q", q, T, self.num_q_heads)
             if q_out is None:
-                q_out = torch.empty((T, self.num_q_heads, self.head_dim), dtype=self.dtype, device=q.device)
-            qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
+                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads)
+            else:
+                qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
         if k is not None:
             kp, ks = self._rows("k", k, T, self.num_kv_heads)
             if k_out is None:
-                k_out = torch.empty((T, self.num_kv_heads, self.head_dim), dtype=self.dtype, device=k.device)
-            ko, kos = self._rows("k_out", k_out, T, self.num_kv_heads)
+                k_out, ko, kos = self._new_rows(k, T, self.num_kv_heads)
+            else:
+                ko, kos = self._rows("k_out", k_out, T, self.num_kv_heads)
         st = self._lib.moe_attn_rotate(self.handle, qp, qs, kp, ks, self._ints("positions", positions, T), T, qo, qos,
-                                       ko, kos, _stream_handle(stream))
+                                       ko, kos, self._stream(stream, positions))
         if st:
             capi.check(st, "moe_attn_rotate")
         return q_out, k_out
@@ -134,12 +151,13 @@ class PagedAttention:
         if q is not None:
             qp, qs = self._rows("q", q, T, self.num_q_heads)
             if q_out is None:
-                q_out = torch.empty((T, self.num_q_heads, self.head_dim), dtype=self.dtype, device=q.device)
-            qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
+                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads)
+            else:
+                qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
         kp, ks = self._rows("k", k, T, self.num_kv_heads)
         vp, vs = self._rows("v", v, T, self.num_kv_heads)
         st = self._lib.moe_attn_append(self.handle, qp, qs, kp, ks, vp, vs, self._ints("positions", positions, T),
-                                       self._ints("slots", slots, T), T, qo, qos, _stream_handle(stream))
+                                       self._ints("slots", slots, T), T, qo, qos, self._stream(stream, positions))
         if st:
             capi.check(st, "moe_attn_append")
         return q_out
@@ -158,8 +176,9 @@ class PagedAttention:
         T, B = q.shape[0], seq_lens.shape[0]
         qp, qs = self._rows("q", q, T, self.num_q_heads)
         if out is None:
-            out = torch.empty((T, self.num_q_heads, self.head_dim), dtype=self.dtype, device=q.device)
-        op, os_ = self._rows("out", out, T, self.num_q_heads)
+            out, op, os_ = self._new_rows(q, T, self.num_q_heads)
+        else:
+            op, os_ = self._rows("out", out, T, self.num_q_heads)
         if lse is None and return_lse:
             lse = torch.empty((T, self.num_q_heads), dtype=torch.float32, device=q.device)
         if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
@@ -182,7 +201,7 @@ class PagedAttention:
                                       self._ints("seq_lens", seq_lens, B), max_seq_len, bt, ts, prefix_len, pp,
                                       int(bool(causal)))
         st = self._lib.moe_attn_forward(self.handle, qp, qs, ctypes.byref(batch), op, os_, _ptr(lse),
-                                        _stream_handle(stream))
+                                        self._stream(stream, q))
         if st:
             capi.check(st, "moe_attn_forward")
         return (out, lse) if return_lse else out

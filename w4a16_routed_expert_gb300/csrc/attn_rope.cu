@@ -18,6 +18,8 @@
 // its top 32 bits as a signed number give an angle in [-pi, pi), where the
 // hardware sine and cosine are within 2^-21.4 absolute, far inside the 16-bit
 // rounding of the result (2^-12 relative).
+#include <algorithm>
+
 #include "attn_dev.cuh"
 
 namespace moe {
@@ -36,158 +38,169 @@ struct Words<4> {
   using type = uint2;
 };
 
+// (x, y) products in pairs
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return ffma2(a, b, make_float2(0.f, 0.f)); }
+
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, int W, int n_chunks) {
+__global__ void __launch_bounds__(kRopeThreads, 4) k_rope(const RopeArgs a, int W, int cq, int ck, int n_chunks) {
   using Vec = typename Words<VEC>::type;
   constexpr int NW = VEC / 2;
-  constexpr int U = 4;  // heads in flight per group
+  constexpr int U = 2;  // heads in flight per group of lanes (4: 10% slower, fewer warps fit)
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long task = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int t = (int)(task / n_chunks);
+  const int task = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)((unsigned)task / (unsigned)n_chunks);
   if (t >= a.T) return;
-  const int chunk = (int)(task - (long long)t * n_chunks);
-  const int gl = lane & (W - 1), grp = lane / W, ngrp = 32 / W;
+  int c = task - t * n_chunks;
+  const int sec = c < cq ? 0 : c < cq + ck ? 1 : 2;  // queries, keys, values
+  c -= sec == 0 ? 0 : sec == 1 ? cq : cq + ck;
+  const int h0 = c * a.heads_per_warp, n = min(a.heads_per_warp, (sec == 0 ? a.Hq : a.Hk) - h0);
+  const int ngrp = 32 / W, gl = lane & (W - 1), grp = lane / W;
   const int d0 = gl * VEC;
-  const bool act = d0 < a.D;
+  const bool act = d0 < a.D, rot = d0 < a.rotary;
 
-  // this token's cosines and sines for the lane's elements
-  const int half = a.rotary >> 1;
-  float C0[VEC], S0[VEC];
-  {
-    const uint64_t pos = (uint64_t)(int64_t)__ldg(a.positions + t);
+  // the first heads are on their way while the angles are worked out
+  const T* src = sec == 0 ? static_cast<const T*>(a.q) + (long long)t * a.q_stride
+                          : sec == 1 ? static_cast<const T*>(a.k) + (long long)t * a.k_stride
+                                     : static_cast<const T*>(a.v) + (long long)t * a.v_stride;
+  const int sstep = ngrp * a.D;
+  src += (h0 + grp) * a.D + d0;
+  Vec raw[U];
+  auto load = [&](int i) {  // heads i, i + ngrp, ...
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int d = d0 + e;
-      C0[e] = 1.f;
-      S0[e] = 0.f;
-      if (d < a.rotary) {
-        const bool second = a.interleaved ? (d & 1) : d >= half;
-        const int i = a.interleaved ? d >> 1 : (second ? d - half : d);
-        const int32_t turn = (int32_t)(uint32_t)((pos * __ldg(a.freq + i)) >> 32);
-        float sn, cs;
-        __sincosf((float)turn * 1.46291807926715968e-9f, &sn, &cs);  // 2 pi / 2^32
-        C0[e] = cs * a.m;
-        S0[e] = (second ? sn : -sn) * a.m;
-      }
+    for (int u = 0; u < U; ++u) {
+      raw[u] = Vec{};
+      if (act && i + u * ngrp + grp < n) raw[u] = *reinterpret_cast<const Vec*>(src + u * sstep);
     }
-  }
-  const bool split = !a.interleaved && a.rotary > 0;  // pairs in two lanes
-  int partner = lane;
-  if (split && d0 < a.rotary) partner = d0 < half ? lane + half / VEC : lane - half / VEC;
+    src += U * sstep;
+  };
+  load(0);
 
-  // the destination slot in the cache
-  long long slot_base = -1;
-  if (a.slots) {
+  // where they go
+  T* dst;
+  long long hstep = a.D;
+  bool store = act;
+  if (sec == 0) {
+    dst = static_cast<T*>(a.q_out) + (long long)t * a.q_out_stride;
+  } else if (a.slots) {
     const long long slot = __ldg(a.slots + t);
-    if (slot >= a.num_slots) {
-      record_error(a.err, kAttnErrBounds);
-    } else if (slot >= 0) {
-      const long long page = slot / a.page_size;
-      slot_base = page * a.page_stride + (slot - page * a.page_size) * a.slot_stride;
+    if (slot >= a.num_slots) record_error(a.err, kAttnErrBounds);
+    store = store && slot >= 0 && slot < a.num_slots;
+    const int page = store ? (int)slot / a.page_size : 0, at = store ? (int)slot - page * a.page_size : 0;
+    dst = static_cast<T*>(sec == 1 ? a.k_cache : a.v_cache) + page * a.page_stride + at * a.slot_stride;
+    hstep = a.head_stride;
+  } else {
+    dst = static_cast<T*>(a.k_out) + (long long)t * a.k_out_stride;
+  }
+  dst += (h0 + grp) * hstep + d0;
+  hstep *= ngrp;
+
+  if (sec == 2) {  // values go as they are
+#pragma unroll 1
+    for (int i = 0; i < n; i += U * ngrp) {
+      Vec cur[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = raw[u];
+      load(i + U * ngrp);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (store && i + u * ngrp + grp < n) *reinterpret_cast<Vec*>(dst) = cur[u];
+        dst += hstep;
+      }
     }
+    return;
   }
 
-  const int nq = a.q ? a.Hq : 0, nk = a.k ? a.Hk : 0, nv = a.slots ? a.Hk : 0;
-  const int h_begin = chunk * a.heads_per_warp, h_end = min(h_begin + a.heads_per_warp, nq + nk + nv);
-  for (int sec = 0; sec < 2; ++sec) {
-    const int lo = max(h_begin, sec ? nq : 0), hi = min(h_end, sec ? nq + nk : nq);
-    if (lo >= hi) continue;
-    const float* w = sec ? a.k_norm : a.q_norm;
-    const T* src = sec ? static_cast<const T*>(a.k) + (long long)t * a.k_stride
-                       : static_cast<const T*>(a.q) + (long long)t * a.q_stride;
-    T* dst;
-    long long hstep = a.D;
-    bool store = act;
-    if (!sec) {
-      dst = static_cast<T*>(a.q_out) + (long long)t * a.q_out_stride;
-    } else if (a.slots) {
-      dst = static_cast<T*>(a.k_cache) + slot_base;
-      hstep = a.head_stride;
-      store = store && slot_base >= 0;
+  // this token's cosines and sines for the lane's elements, with the norm's
+  // weights of the elements and of their pairs' other elements
+  const int half = a.rotary >> 1;
+  const bool split = !a.interleaved && a.rotary > 0;  // pairs in two lanes
+  const bool second = d0 >= half;                     // then: the lane holds second elements
+  const int partner = split && rot ? (second ? lane - half / VEC : lane + half / VEC) : lane;
+  float2 C[NW], S[NW];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    C[i] = make_float2(1.f, 1.f);
+    S[i] = make_float2(0.f, 0.f);
+  }
+  if (rot) {
+    const uint64_t pos = (uint64_t)(int64_t)__ldg(a.positions + t);
+    auto angle = [&](uint64_t f, float* sn, float* cs) {
+      __sincosf((float)(int32_t)(uint32_t)((pos * f) >> 32) * 1.46291807926715968e-9f, sn, cs);  // 2 pi / 2^32
+    };
+    if (a.interleaved) {
+      const uint64_t* f = a.freq + (d0 >> 1);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        float sn, cs;
+        angle(__ldg(f + i), &sn, &cs);
+        C[i] = make_float2(cs * a.m, cs * a.m);
+        S[i] = make_float2(-sn * a.m, sn * a.m);
+      }
     } else {
-      dst = static_cast<T*>(a.k_out) + (long long)t * a.k_out_stride;
-    }
-    const int h0 = sec ? nq : 0;
-    float C[VEC], S[VEC];
+      const ulonglong2* f = reinterpret_cast<const ulonglong2*>(a.freq + (second ? d0 - half : d0));
+      const float sm = second ? a.m : -a.m;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      C[e] = C0[e];
-      S[e] = S0[e];
-      if (w && act) {
-        const int d = d0 + e;
-        int pd = d;
-        if (d < a.rotary) pd = a.interleaved ? d ^ 1 : (d < half ? d + half : d - half);
-        C[e] *= __ldg(w + d);
-        S[e] *= __ldg(w + pd);
-      }
-    }
-    for (int h = lo; h < hi; h += ngrp * U) {
-      Vec raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u * ngrp + grp;
-        raw[u] = Vec{};
-        if (act && hh < hi) raw[u] = *reinterpret_cast<const Vec*>(src + (long long)(hh - h0) * a.D + d0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u * ngrp + grp;
-        const uint32_t* rw = reinterpret_cast<const uint32_t*>(&raw[u]);
-        float x[VEC], y[VEC];
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          const float2 f = Half16<T>::unpack(rw[i]);
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
-          if (split) {
-            const float2 p = Half16<T>::unpack(__shfl_sync(0xffffffffu, rw[i], partner));
-            y[2 * i] = p.x;
-            y[2 * i + 1] = p.y;
-          } else {
-            y[2 * i] = f.y;
-            y[2 * i + 1] = f.x;
-          }
-        }
-        float r = 1.f;
-        if (w) {
-          for (int o = W >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          r = rsqrtf(ss / (float)a.D + a.eps);
-        }
-        Vec res;
-        uint32_t* ow = reinterpret_cast<uint32_t*>(&res);
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          // an element that is not rotated keeps its value whatever stands beside it
-          const float s0 = d0 + 2 * i < a.rotary ? y[2 * i] * S[2 * i] : 0.f;
-          const float s1 = d0 + 2 * i + 1 < a.rotary ? y[2 * i + 1] * S[2 * i + 1] : 0.f;
-          ow[i] = Half16<T>::pack(r * fmaf(x[2 * i], C[2 * i], s0), r * fmaf(x[2 * i + 1], C[2 * i + 1], s1));
-        }
-        if (store && hh < hi) *reinterpret_cast<Vec*>(dst + (long long)(hh - h0) * hstep + d0) = res;
+      for (int i = 0; i < NW; ++i) {
+        const ulonglong2 ff = __ldg(f + i);
+        float2 sn, cs;
+        angle(ff.x, &sn.x, &cs.x);
+        angle(ff.y, &sn.y, &cs.y);
+        C[i] = make_float2(cs.x * a.m, cs.y * a.m);
+        S[i] = make_float2(sn.x * sm, sn.y * sm);
       }
     }
   }
-  // values: copied to the cache as they are
-  if (nv && slot_base >= 0) {
-    const int h0 = nq + nk;
-    const int lo = max(h_begin, h0);
-    const T* src = static_cast<const T*>(a.v) + (long long)t * a.v_stride;
-    T* dst = static_cast<T*>(a.v_cache) + slot_base;
-    for (int h = lo; h < h_end; h += ngrp * U) {
-      Vec raw[U];
+  const float* w = sec == 0 ? a.q_norm : a.k_norm;
+  if (w && act) {
+    const float* wp = w + (!split || !rot ? d0 : second ? d0 - half : d0 + half);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u * ngrp + grp;
-        if (act && hh < h_end) raw[u] = *reinterpret_cast<const Vec*>(src + (long long)(hh - h0) * a.D + d0);
-      }
+    for (int i = 0; i < NW; ++i) {
+      const float2 wd = __ldg(reinterpret_cast<const float2*>(w + d0) + i);
+      float2 wo = __ldg(reinterpret_cast<const float2*>(wp) + i);
+      if (a.interleaved) wo = make_float2(wd.y, wd.x);
+      C[i] = mul2(C[i], wd);
+      S[i] = mul2(S[i], wo);
+    }
+  }
+  const float inv_d = 1.f / (float)a.D;
+
+#pragma unroll 1
+  for (int i = 0; i < n; i += U * ngrp) {
+    Vec cur[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u * ngrp + grp;
-        if (act && hh < h_end) *reinterpret_cast<Vec*>(dst + (long long)(hh - h0) * a.head_stride + d0) = raw[u];
+    for (int u = 0; u < U; ++u) cur[u] = raw[u];
+    load(i + U * ngrp);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t* rw = reinterpret_cast<const uint32_t*>(&cur[u]);
+      float2 x[NW];
+      float r = 1.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) x[k] = Half16<T>::unpack(rw[k]);
+      if (w) {
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) s2 = ffma2(x[k], x[k], s2);
+        float ss = s2.x + s2.y;
+        for (int o = W >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = rsqrtf(fmaf(ss, inv_d, a.eps));
       }
+      const float2 r2 = make_float2(r, r);
+      Vec res;
+      uint32_t* ow = reinterpret_cast<uint32_t*>(&res);
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        float2 y = make_float2(x[k].y, x[k].x);
+        if (split) y = Half16<T>::unpack(__shfl_sync(0xffffffffu, rw[k], partner));
+        // an element that is not rotated keeps its value whatever stands beside it
+        if (!rot) y = make_float2(0.f, 0.f);
+        const float2 v = mul2(r2, ffma2(x[k], C[k], mul2(y, S[k])));
+        ow[k] = Half16<T>::pack(v.x, v.y);
+      }
+      if (store && i + u * ngrp + grp < n) *reinterpret_cast<Vec*>(dst) = res;
+      dst += hstep;
     }
   }
 }
@@ -199,20 +212,23 @@ cudaError_t launch(const RopeArgs& in, int num_sms, cudaStream_t s, bool pdl) {
   const int vec = (!a.interleaved && a.rotary % 16 != 0) ? 4 : 8;
   int W = 1;
   while (W * vec < a.D) W <<= 1;
-  const int heads = (a.q ? a.Hq : 0) + (a.k ? a.Hk : 0) + (a.slots ? a.Hk : 0);
-  // One warp takes one token's heads (its sines and cosines are computed
-  // once); with few tokens the heads are spread over more warps until the
-  // card has about 32 warps per SM.
+  const int nq = a.q ? a.Hq : 0, nk = a.k ? a.Hk : 0, nv = a.slots ? a.Hk : 0;
+  // One warp takes a token's query, key or value heads, whose sines and
+  // cosines it computes once; with few tokens the heads are spread over more
+  // warps until the card has about 24 warps per SM.
   const int step = 32 / W;
-  int per = heads;
-  while (per > step && (long long)a.T * ((heads + per - 1) / per) < 32LL * num_sms) per = (per + 1) / 2;
+  auto chunks = [](int n, int per) { return (n + per - 1) / per; };
+  int per = std::max(nq, nk);
+  while (per > step &&
+         (long long)a.T * (chunks(nq, per) + chunks(nk, per) + chunks(nv, per)) < 24LL * num_sms)
+    per = (per + 1) / 2;
   per = (per + step - 1) / step * step;
   a.heads_per_warp = per;
-  const int n_chunks = (heads + per - 1) / per;
+  const int cq = chunks(nq, per), ck = chunks(nk, per), n_chunks = cq + ck + chunks(nv, per);
   const long long warps = (long long)a.T * n_chunks;
   const dim3 grid((unsigned)((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
-  if (vec == 8) return launch_ex(k_rope<T, 8>, grid, dim3(kRopeThreads), 0, s, pdl, a, W, n_chunks);
-  return launch_ex(k_rope<T, 4>, grid, dim3(kRopeThreads), 0, s, pdl, a, W, n_chunks);
+  if (vec == 8) return launch_ex(k_rope<T, 8>, grid, dim3(kRopeThreads), 0, s, pdl, a, W, cq, ck, n_chunks);
+  return launch_ex(k_rope<T, 4>, grid, dim3(kRopeThreads), 0, s, pdl, a, W, cq, ck, n_chunks);
 }
 
 }  // namespace
