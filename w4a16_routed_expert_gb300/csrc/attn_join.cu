@@ -13,65 +13,95 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// DP / 8 lanes to a row, 8 values each
+// A warp a row, DP / 8 lanes to a partial and 8 values a lane, so 2 (4 at
+// DP 64) partials side by side; a partial's maximum, sum and row are loaded
+// together and taken into a running result, which the lane groups then join.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
-  constexpr int W = DP / 8;
+__global__ void __launch_bounds__(kJoinThreads, 4) k_attn_join(const JoinArgs j) {
+  constexpr int W = DP / 8, G = 32 / W;
+  constexpr int U = 4;  // partials in flight per lane group
   pdl_trigger();
   pdl_wait();
   const AttnArgs& a = j.a;
-  const int gl = threadIdx.x & (W - 1);
-  const long long row = ((long long)blockIdx.x * kJoinThreads + threadIdx.x) / W;
-  const bool in = row < (long long)a.T * a.Hq;
+  const int lane = threadIdx.x & 31, gl = lane & (W - 1), grp = lane / W;
+  const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  if (row >= (long long)a.T * a.Hq) return;
 
   // the row's partials of the prefix and of its own keys; the words go back to
   // zero for the next forward
   int2 ip = make_int2(0, 0), io = make_int2(0, 0);
-  if (in && j.prefix_step) ip = j.info_prefix[row];
-  if (in && j.own_step) io = j.info_own[row];
+  if (j.prefix_step) ip = j.info_prefix[row];
+  if (j.own_step) io = j.info_own[row];
   __syncwarp();
-  if (in && gl == 0) {
+  if (lane == 0) {
     if (j.prefix_step) j.info_prefix[row] = make_int2(0, 0);
     if (j.own_step) j.info_own[row] = make_int2(0, 0);
   }
-  if (!in || ip.y < 0 || io.y < 0) return;  // stored by the one block that had all its keys
+  if (ip.y < 0 || io.y < 0) return;  // stored by the one block that had all its keys
   const int n = ip.y + io.y;
-  auto part = [&](int i) {
-    return i < ip.y ? (long long)ip.x + (long long)i * j.prefix_step
-                    : (long long)io.x + (long long)(i - ip.y) * j.own_step;
-  };
-  const unsigned lanes = (W == 16 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & ~(W - 1));
-  float m = -INFINITY;
-  for (int i = gl; i < n; i += W) m = fmaxf(m, j.part_ml[part(i)].x);
-#pragma unroll
-  for (int o = W >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float o[8] = {};
   const bool act = gl * 8 < a.D;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long at = part(i);
-    const float2 v = j.part_ml[at];
-    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-    if (act) {
-      p = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8);
-      q = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8 + 4);
+  float m = -INFINITY, l = 0.f;
+  float o[8] = {};
+  // m and the running sums move to max(m, mi); -inf stays -inf
+  auto scale_to = [&](float mn, float mi) { return mi == mn ? 1.f : exp2_fast(mi - mn); };
+#pragma unroll 1
+  for (int i = grp; i < n; i += G * U) {
+    float2 v[U];
+    float4 p[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = i + u * G;
+      v[u] = make_float2(-INFINITY, 0.f);
+      p[u] = q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n) {
+        const long long at = k < ip.y ? (long long)ip.x + (long long)k * j.prefix_step
+                                      : (long long)io.x + (long long)(k - ip.y) * j.own_step;
+        v[u] = j.part_ml[at];
+        if (act) {
+          p[u] = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8);
+          q[u] = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8 + 4);
+        }
+      }
     }
-    const float w = exp2_fast(v.x - ref);
-    l = fmaf(w, v.y, l);
-    o[0] = fmaf(w, p.x, o[0]);
-    o[1] = fmaf(w, p.y, o[1]);
-    o[2] = fmaf(w, p.z, o[2]);
-    o[3] = fmaf(w, p.w, o[3]);
-    o[4] = fmaf(w, q.x, o[4]);
-    o[5] = fmaf(w, q.y, o[5]);
-    o[6] = fmaf(w, q.z, o[6]);
-    o[7] = fmaf(w, q.w, o[7]);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, v[u].x);
+    const float f = scale_to(mn, m);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = scale_to(mn, v[u].x);
+      l = fmaf(w, v[u].y, l);
+      o[0] = fmaf(w, p[u].x, o[0]);
+      o[1] = fmaf(w, p[u].y, o[1]);
+      o[2] = fmaf(w, p[u].z, o[2]);
+      o[3] = fmaf(w, p[u].w, o[3]);
+      o[4] = fmaf(w, q[u].x, o[4]);
+      o[5] = fmaf(w, q[u].y, o[5]);
+      o[6] = fmaf(w, q[u].z, o[6]);
+      o[7] = fmaf(w, q[u].w, o[7]);
+    }
+  }
+#pragma unroll
+  for (int s = W; s < 32; s <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, s), l2 = __shfl_xor_sync(0xffffffffu, l, s);
+    const float mn = fmaxf(m, m2), f = scale_to(mn, m), f2 = scale_to(mn, m2);
+    // the lower group's share first, on both sides
+    const bool lower = (lane & s) == 0;
+    l = lower ? fmaf(l2, f2, l * f) : fmaf(l, f, l2 * f2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float o2 = __shfl_xor_sync(0xffffffffu, o[e], s);
+      o[e] = lower ? fmaf(o2, f2, o[e] * f) : fmaf(o[e], f, o2 * f2);
+    }
+    m = mn;
   }
   const float inv = inverse_sum(l);  // a row that sees no key: zeros
   const int t = (int)(row / a.Hq), hq = (int)(row - (long long)t * a.Hq);
-  if (act) {
+  if (act && grp == 0) {
     uint4 r;
     r.x = Half16<T>::pack(o[0] * inv, o[1] * inv);
     r.y = Half16<T>::pack(o[2] * inv, o[3] * inv);
@@ -79,13 +109,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
     r.w = Half16<T>::pack(o[6] * inv, o[7] * inv);
     *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)t * a.out_stride + (long long)hq * a.D + gl * 8) = r;
   }
-  if (a.lse && gl == 0) a.lse[row] = log_sum<T>(m, l);
+  if (a.lse && lane == 0) a.lse[row] = log_sum<T>(m, l);
 }
 
 template <typename T>
 cudaError_t launch(const JoinArgs& j, cudaStream_t s, bool pdl) {
-  const long long threads = (long long)j.a.T * j.a.Hq * (j.DP / 8);
-  const dim3 grid((unsigned)((threads + kJoinThreads - 1) / kJoinThreads));
+  const long long rows = (long long)j.a.T * j.a.Hq;
+  const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   return j.DP == 128 ? launch_ex(k_attn_join<T, 128>, grid, dim3(kJoinThreads), 0, s, pdl, j)
                      : launch_ex(k_attn_join<T, 64>, grid, dim3(kJoinThreads), 0, s, pdl, j);
 }
