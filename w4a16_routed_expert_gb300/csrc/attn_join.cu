@@ -17,9 +17,9 @@ constexpr int kJoinThreads = 256;
 // DP 64) partials side by side; a partial's maximum, sum and row are loaded
 // together and taken into a running result, which the lane groups then join.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kJoinThreads, 4) k_attn_join(const JoinArgs j) {
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
   constexpr int W = DP / 8, G = 32 / W;
-  constexpr int U = 4;  // partials in flight per lane group
+  constexpr int U = 2;  // partials in flight per lane group
   pdl_trigger();
   pdl_wait();
   const AttnArgs& a = j.a;
