@@ -223,6 +223,12 @@ FORWARD = {  # dtype, Hq, Hk, D, page, order, query lengths, own keys, prefix, c
     "a late chunk": (F16, 8, 1, 64, 128, "slot", [100, 33], [1000, 33], 0, True),
     "a long prefix for many": (BF16, 16, 2, 128, 64, "slot", [1] * 40, [i for i in range(40)], 5003, True),
     "a long context for one": (F16, 8, 8, 128, 64, "slot", [1], [9001], 0, True),
+    "chunks behind a prefix, blocks of their own": (BF16, 16, 2, 128, 16, "head", [70, 33, 40], [80, 33, 300], 333, True),
+    "chunks behind a prefix, no causality": (F16, 8, 1, 96, 32, "slot", [40, 50], [3, 200], 129, False),
+    "a chunk that sees the prefix alone": (F16, 4, 1, 64, 16, "slot", [100], [40], 77, True),
+    "short chunks behind a prefix": (F16, 8, 2, 64, 64, "slot", [20, 9, 33], [20, 70, 500], 600, True),
+    "two thousand tokens": (F16, 2, 1, 64, 16, "slot", [2000], [2100], 130, True),
+    "as many groups as there are keys": (BF16, 64, 64, 128, 16, "slot", [1] * 12, [i % 5 for i in range(12)], 0, True),
     "very unequal": (F16, 16, 4, 128, 32, "head", [1] * 9, [1, 4100, 2, 0, 3, 64, 65, 8, 700], 0, True),
 }
 
@@ -486,3 +492,45 @@ def test_refusals():
     with pytest.raises(ValueError):
         a.rotate(x.half(), None, torch.zeros(2, dtype=torch.int64, device="cuda"))
     a.sync()
+
+
+# ----------------------------------------------------------- used together
+
+def test_decoder_blocks_behind_a_shared_prompt():
+    """Two blocks (append, forward, routed experts) decode behind a prompt that
+    all sequences share, and behind copies of it in every sequence's own pages.
+    Only the attention is computed another way, so the hidden states agree to
+    the rounding of the 16-bit probabilities and outputs, block after block;
+    a token whose routing stands on a tie may pick other experts."""
+    import importlib.util
+    import os
+
+    from w4a16_routed_expert_gb300 import synth
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "shared_prefix_decode.py")
+    spec = importlib.util.spec_from_file_location("shared_prefix_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    seqs, prompt_len, steps = 9, 301, 3
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    H = synth.TINY.hidden
+    prompt = torch.randn(prompt_len, H, generator=gen, device="cuda").half()
+    first = torch.randn(seqs, H, generator=gen, device="cuda").half()
+    runs = []
+    for share in (True, False):
+        d = ex.SharedPrefixDecoder(synth.TINY, n_blocks=2, q_heads=8, kv_heads=2, head_dim=64, seqs=seqs,
+                                   prompt_len=prompt_len, max_new=steps, share=share)
+        out = [d.prefill(prompt)]
+        x = first
+        for _ in range(steps):
+            out.append(d.step(x))
+            x = ex.Block.norm(out[-1])
+        d.sync()
+        runs.append([o.double().cpu() for o in out])
+    assert torch.equal(runs[0][0], runs[1][0])  # the prompt's own pass is the same in both
+    for a, b in zip(*runs):
+        assert torch.isfinite(a).all()
+        # each step: probabilities and outputs rounded to 2^-11, then two blocks of
+        # products of unit gain; a few times that, relative to the states' size
+        rel = (a - b).norm(dim=1) / b.norm(dim=1)
+        assert (rel < 0.01).double().mean() >= 0.85 and rel.median() < 0.005, rel
