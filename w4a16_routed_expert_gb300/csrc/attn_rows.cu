@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               mma16816<T>(sv[m][1], qf, kf[2], kf[3]);
             }
           }
-          uint32_t pf[MT][4];
+          uint32_t pf[MT][4], pl[MT][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (k0 + 16 > all_see) {
@@ -317,10 +317,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                   l[m][e] += p[n][2 * e + f];
                 }
             }
-            pf[m][0] = Half16<T>::pack(p[0][0], p[0][1]);
-            pf[m][1] = Half16<T>::pack(p[0][2], p[0][3]);
-            pf[m][2] = Half16<T>::pack(p[1][0], p[1][1]);
-            pf[m][3] = Half16<T>::pack(p[1][2], p[1][3]);
+            // the weights as two 16-bit numbers, the rounded one and what it
+            // leaves: with few rows their rounding would not average out, and
+            // the second product hides under the copies
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const float w0 = p[f >> 1][2 * (f & 1)], w1 = p[f >> 1][2 * (f & 1) + 1];
+              pf[m][f] = Half16<T>::pack(w0, w1);
+              const float2 r = Half16<T>::unpack(pf[m][f]);
+              pl[m][f] = Half16<T>::pack(w0 - r.x, w1 - r.y);
+            }
           }
 #pragma unroll
           for (int nn = 0; nn < DP / 16; ++nn) {
@@ -333,6 +339,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int m = 0; m < MT; ++m) {
               mma16816<T>(o[m][2 * nn], pf[m], vf[0], vf[1]);
               mma16816<T>(o[m][2 * nn + 1], pf[m], vf[2], vf[3]);
+              mma16816<T>(o[m][2 * nn], pl[m], vf[0], vf[1]);
+              mma16816<T>(o[m][2 * nn + 1], pl[m], vf[2], vf[3]);
             }
           }
           if (here < 16) fence_async_smem();  // the zeros before the stage's next copies
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               if (t4 == 0) {
                 if (!done)
-                  ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
+                  ln.part_ml[cur.prow + r] = make_float4(mt[m][e], lt[m][e], lt[m][e], 0.f);
                 else if (a.lse)
                   a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mt[m][e], lt[m][e]);
                 if (cur.parts) write_info(a, ln, cur, r, at);

@@ -43,6 +43,9 @@ constexpr int kKT = kTileKeyTile;
 constexpr int kThreads = 11 * 32;
 constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLanded = 10;
 constexpr int kMaxStages = 8;
+// A row's weights of one tile: a reference at the maximum gives at most 128 *
+// 2^7 (FP16, ProbBias), and below 2^15 no FP16 weight overflows.
+constexpr float kSumMost = 32768.f;
 
 struct SmemPlan {
   uint32_t ring, bars, seg, misc, off, bytes;
@@ -67,7 +70,9 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 
-template <typename T, int DP>
+// RSUM: the quotient takes the sum of the weights as they were rounded for the
+// products (few rows, see launch_attn_tile).
+template <typename T, int DP, bool RSUM>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2) {
@@ -364,14 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot_i = 0;
     int vst = 0;  // ring stage of the next key tile, and its phase
     uint32_t vph = 0;
-    // the next part, in its slot; taken over with take_segment
+    // A part's description stays in its slot until the part is done: `cur` is
+    // read where it is needed, and gives no registers to what the tiles' loop
+    // does not use.
     auto peek_segment = [&]() {
       const bool got = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], gph, abort_flag, a.err));
       return got && segs[slot_i].tiles > 0;
     };
-    auto take_segment = [&](Segment* s) {
-      *s = segs[slot_i];
-      arrive(&seg_empty[slot_i]);
+    auto next_slot = [&]() {
       if (++slot_i == kSegSlots) {
         slot_i = 0;
         gph ^= 1u;
@@ -383,30 +388,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_smem();
       arrive(&q_full[t]);
     };
-    Segment s;
     bool ok = true, some = peek_segment();
+    const Segment* cur = &segs[slot_i];
     if (some) {
-      if (uses(&segs[slot_i])) {
-        load_q(&segs[slot_i]);
+      if (uses(cur)) {
+        load_q(cur);
         q_arrive();
       }
-      take_segment(&s);
+      next_slot();
     }
     while (some) {
-      const bool used = uses(&s);
+      const bool used = uses(cur);
       bool more = false, more_used = false;  // there is another part, and this row tile has rows in it
-      const bool any_row = t * 128 + (warp & 3) * 32 < s.rows;  // this warp has a row
+      const bool any_row = t * 128 + (warp & 3) * 32 < cur->rows;
+      const int tiles = cur->tiles;  // this warp has a row
       float mref = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f);
+      // sums of the weights, and (RSUM) of the weights as rounded: the quotient
+      // takes the latter, so that a key that stands alone gives its value
+      // exactly, the logarithm the former
+      float2 l2 = make_float2(0.f, 0.f), lr2 = l2;
       if (used) {
-        const int row = s.row0 + min(r, s.rows - 1);
-        const int lim = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
-        const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
+        const int row = cur->row0 + min(r, cur->rows - 1);
+        const int lim = cur->b < 0 ? cur->klen : keys_seen(a, cur->klen, cur->n, row / a.g);
+        const int all_see = cur->b < 0 ? cur->klen : keys_seen(a, cur->klen, cur->n, cur->row0 / a.g);
+        const int tile0 = cur->tile, front = cur->front, nkeys = cur->nkeys;
 #pragma unroll 1
-        for (int i = 0; i < s.tiles; ++i) {
-          const bool pre = s.tile + i < s.front;  // a tile of the prefix before own keys
-          const int k0 = (s.tile + i - (pre ? 0 : s.front)) * kKT;
-          const int nk = pre ? a.prefix_len : s.nkeys;
+        for (int i = 0; i < tiles; ++i) {
+          const bool pre = tile0 + i < front;  // a tile of the prefix before own keys
+          const int k0 = (tile0 + i - (pre ? 0 : front)) * kKT;
+          const int nk = pre ? a.prefix_len : nkeys;
           const bool got = mbar_wait(&s_full[t], sph, abort_flag, a.err);
           sph ^= 1u;
           if (!__all_sync(0xffffffffu, got)) {
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (i + 1 == s.tiles) {
+          if (i + 1 == tiles) {
             // this part's last Q K^T has completed: the next one's queries may
             // come in under its softmax
             more = peek_segment();
@@ -425,12 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool edge = k0 + kKT > (pre ? a.prefix_len : all_see);
             const int seen = pre ? a.prefix_len : lim;
             uint32_t p[64];
-            float2 lt;
-            // The weights are taken against the reference maximum as it stands
-            // while the tile's own maximum is still being found, so neither
-            // waits for the other; only when a row passes the reference by
-            // more than kLazy is it moved and the tile, still in tensor
-            // memory, done again. The first tile sets it beforehand.
+            float2 lt, lrt;
+            // The weights are taken against the reference maximum as it stands;
+            // a tile's own maximum is not looked for. Only when a row's weights
+            // add up to more than kSumMost (none can pass it then, so none
+            // overflows) is the reference moved to the maximum and the tile,
+            // still in tensor memory, done again. The first tile sets it
+            // beforehand.
             auto mask = [&](uint32_t(&v)[32], int c) {
               if (edge) {
 #pragma unroll
@@ -438,30 +449,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (k0 + c * 32 + e >= seen) v[e] = 0xff800000u;
               }
             };
-            float m = -INFINITY;
             bool move = i == 0;
-            if (move) {
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld32(ts + c * 32, v);
-                tmem_ld_wait_for(v);
-                mask(v, c);
-                float mx[2] = {m, -INFINITY};
-#pragma unroll
-                for (int e = 0; e < 32; ++e) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(v[e]));
-                m = fmaxf(mx[0], mx[1]);
-              }
-              m *= sc;
-            }
 #pragma unroll 1
             while (true) {
               if (move) {
-                const float mn = fmaxf(mref, m);
+                float m = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t v[32];
+                  tmem_ld32(ts + c * 32, v);
+                  tmem_ld_wait_for(v);
+                  mask(v, c);
+                  float mx[2] = {m, -INFINITY};
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(v[e]));
+                  m = fmaxf(mx[0], mx[1]);
+                }
+                const float mn = fmaxf(mref, m * sc);
                 const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
                 mref = mn;
                 l2.x *= f;
                 l2.y *= f;
+                lr2.x *= f;
+                lr2.y *= f;
                 if (i > 0) {
 #pragma unroll 1
                   for (int c = 0; c < DP / 32; ++c) {
@@ -476,8 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
               const float2 nref = make_float2(-ref, -ref);
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-              lt = make_float2(0.f, 0.f);
+              lt = lrt = make_float2(0.f, 0.f);
               uint32_t sr[2][32];
               tmem_ld32(ts, sr[0]);
               tmem_ld_wait_for(sr[0]);
@@ -487,22 +496,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < 3) tmem_ld32(ts + (c + 1) * 32, sr[(c + 1) & 1]);
                 mask(v, c);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-#pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   float2 w = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, nref);
                   w.x = exp2_fast(w.x);
                   w.y = exp2_fast(w.y);
                   lt = fadd2(lt, w);
                   p[c * 16 + e] = Half16<T>::pack(w.x, w.y);
+                  if (RSUM) lrt = fadd2(lrt, Half16<T>::unpack(p[c * 16 + e]));
                 }
                 if (c < 3) tmem_ld_wait_for(sr[(c + 1) & 1]);
               }
-              m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-              move = __any_sync(0xffffffffu, m > mref + kLazy);
+              move = __any_sync(0xffffffffu, lt.x + lt.y > kSumMost);
               if (!move) break;
             }
             l2 = fadd2(l2, lt);
+            lr2 = fadd2(lr2, lrt);
             tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
             tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
             tmem_st_wait();
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       {
-        const int z = vst + 2 * s.tiles;
+        const int z = vst + 2 * tiles;
         vph ^= (uint32_t)(z / stages) & 1u;
         vst = z % stages;
       }
@@ -551,17 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any_row) {
-          const bool done = whole(ln, s);
-          const int2 at = s.parts ? row_place(a, s, r) : make_int2(0, 0);
-          const float l = l2.x + l2.y, inv = inverse_sum(l);
-          float* dst = ln.part_o + (long long)(s.prow + r) * DP;
+          const bool done = whole(ln, *cur);
+          const int2 at = cur->parts ? row_place(a, *cur, r) : make_int2(0, 0);
+          const float l = l2.x + l2.y, lr = RSUM ? lr2.x + lr2.y : l, inv = inverse_sum(lr);
+          float* dst = ln.part_o + (long long)(cur->prow + r) * DP;
           T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D;
 #pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(to + c * 32, o);
             tmem_ld_wait_for(o);
-            if (r < s.rows) {
+            if (r < cur->rows) {
               if (!done) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
@@ -578,19 +586,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (r < s.rows) {
+          if (r < cur->rows) {
             if (!done)
-              ln.part_ml[s.prow + r] = make_float2(mref, l);
+              ln.part_ml[cur->prow + r] = make_float4(mref, l, lr, 0.f);
             else if (a.lse)
               a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l);
-            if (s.parts) write_info(a, ln, s, r, at);
+            if (cur->parts) write_info(a, ln, *cur, r, at);
           }
         }
         tc_fence_before();
       }
       if (more_used) q_arrive();
+      arrive(&seg_empty[cur - segs]);
       some = more;
-      if (some) take_segment(&s);
+      cur = &segs[slot_i];
+      if (some) next_slot();
     }
     cp_async_wait_all();  // (none are left unless a wait gave up)
   }
@@ -615,15 +625,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool RSUM>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
                    cudaStream_t s, bool pdl) {
   int stages = kMaxStages;  // as many as fit
   while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
   const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
-  const cudaError_t e = ensure_smem(k_attn_tile<T, DP>, smem);
+  const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM>, smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k_attn_tile<T, DP>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages, box_log2);
+  return launch_ex(k_attn_tile<T, DP, RSUM>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
+                   box_log2);
+}
+
+// A weight's rounding to 16 bits is as large as the output's own. Against
+// 64-bit results the outputs of many rows together are 1.35 times as far off
+// as rounding alone would leave them; a few rows by themselves, with a few
+// hundred keys, up to 1.8 times, or 1.4 with the quotient by the rounded sum,
+// which costs up to 8% (four chunks of 770 tokens: 402 us against 366). Below
+// 4096 rows it is taken.
+template <typename T>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int bl,
+                     cudaStream_t s, bool pdl) {
+  const bool few = (long long)a.T * a.Hq < 4096;
+  if (a.D <= 64)
+    return few ? launch<T, 64, true>(tk, tv, a, ln, bl, s, pdl) : launch<T, 64, false>(tk, tv, a, ln, bl, s, pdl);
+  return few ? launch<T, 128, true>(tk, tv, a, ln, bl, s, pdl) : launch<T, 128, false>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace
@@ -632,9 +658,7 @@ cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const
                              int box_slots, bool bf16, cudaStream_t s, bool pdl) {
   int bl = 4;
   while ((1 << bl) < box_slots) ++bl;
-  if (a.D <= 64)
-    return bf16 ? launch<__nv_bfloat16, 64>(tk, tv, a, ln, bl, s, pdl) : launch<__half, 64>(tk, tv, a, ln, bl, s, pdl);
-  return bf16 ? launch<__nv_bfloat16, 128>(tk, tv, a, ln, bl, s, pdl) : launch<__half, 128>(tk, tv, a, ln, bl, s, pdl);
+  return bf16 ? launch_t<__nv_bfloat16>(tk, tv, a, ln, bl, s, pdl) : launch_t<__half>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace moe
