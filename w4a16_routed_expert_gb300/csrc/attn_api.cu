@@ -28,7 +28,7 @@ struct moe_attn {
   // forward's workspace
   int2* info[2] = {};            // [max_tokens][Hq] of the prefix, of own keys: where a row's partials are
   float* part_o = nullptr;       // [part_rows][DP]
-  float4* part_ml = nullptr;     // [part_rows]
+  float2* part_ml = nullptr;     // [part_rows]
   size_t part_rows = 0;
   int DP = 0;
   int box_rows = 0, box_tile = 0;  // slots of one copy of the few-row and of the tile kernel
@@ -292,7 +292,7 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   if (buffers->k_cache) {
     h->DP = config->head_dim <= 64 ? 64 : 128;
     h->part_rows = 2 * NR + (size_t)h->num_sms * (2 * moe::kRowsMax + moe::kTileRows);
-    bytes += 2 * align256(NR * 8) + align256(h->part_rows * h->DP * 4) + align256(h->part_rows * 16);
+    bytes += 2 * align256(NR * 8) + align256(h->part_rows * h->DP * 4) + align256(h->part_rows * 8);
     h->box_rows = 16;  // the largest box that pages divide into
     while (h->box_rows < moe::kRowsKeyTile && config->page_size % (2 * h->box_rows) == 0) h->box_rows *= 2;
     h->box_tile = h->box_rows;
@@ -328,7 +328,7 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
     };
     for (int i = 0; i < 2; ++i) h->info[i] = reinterpret_cast<int2*>(carve(NR * 8));
     h->part_o = reinterpret_cast<float*>(carve(h->part_rows * h->DP * 4));
-    h->part_ml = reinterpret_cast<float4*>(carve(h->part_rows * 16));
+    h->part_ml = reinterpret_cast<float2*>(carve(h->part_rows * 8));
   }
   uint64_t turns[64] = {};
   if (config->rotary_dim > 0) {

@@ -1,8 +1,7 @@
 // Joins the partial results of one forward: for each (query token, query
 // head) the rows that the blocks left in the workspace (maximum m_i in powers
-// of two, sums l_i and, of the weights as they were rounded, l'_i, output o_i
-// relative to 2^m_i) become
-//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l'_i,  m = max_i m_i,
+// of two, sum l_i, output o_i relative to 2^m_i) become
+//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i,
 //   lse = ln 2 (m + log2 sum_i 2^(m_i - m) l_i) - ln 2 * bias
 // in a fixed order. The partials were just written, so the reads mostly hit
 // L2; what bounds it is the chain of two loads (where the partials are, then
@@ -41,19 +40,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
   if (ip.y < 0 || io.y < 0) return;  // stored by the one block that had all its keys
   const int n = ip.y + io.y;
   const bool act = gl * 8 < a.D;
-  float m = -INFINITY, l = 0.f, lr = 0.f;
+  float m = -INFINITY, l = 0.f;
   float o[8] = {};
   // m and the running sums move to max(m, mi); -inf stays -inf
   auto scale_to = [&](float mn, float mi) { return mi == mn ? 1.f : exp2_fast(mi - mn); };
 #pragma unroll 1
   for (int i = grp; i < n; i += G * U) {
-    float4 v[U];
+    float2 v[U];
     float4 p[U], q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = i + u * G;
       p[u] = q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      v[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      v[u] = make_float2(-INFINITY, 0.f);
       if (k < n) {
         const long long at = k < ip.y ? (long long)ip.x + (long long)k * j.prefix_step
                                       : (long long)io.x + (long long)(k - ip.y) * j.own_step;
@@ -70,14 +69,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
     const float f = scale_to(mn, m);
     m = mn;
     l *= f;
-    lr *= f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] *= f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float w = scale_to(mn, v[u].x);
       l = fmaf(w, v[u].y, l);
-      lr = fmaf(w, v[u].z, lr);
       o[0] = fmaf(w, p[u].x, o[0]);
       o[1] = fmaf(w, p[u].y, o[1]);
       o[2] = fmaf(w, p[u].z, o[2]);
@@ -91,12 +88,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
 #pragma unroll
   for (int s = W; s < 32; s <<= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, s), l2 = __shfl_xor_sync(0xffffffffu, l, s);
-    const float lr2 = __shfl_xor_sync(0xffffffffu, lr, s);
     const float mn = fmaxf(m, m2), f = scale_to(mn, m), f2 = scale_to(mn, m2);
     // the lower group's share first, on both sides
     const bool lower = (lane & s) == 0;
     l = lower ? fmaf(l2, f2, l * f) : fmaf(l, f, l2 * f2);
-    lr = lower ? fmaf(lr2, f2, lr * f) : fmaf(lr, f, lr2 * f2);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float o2 = __shfl_xor_sync(0xffffffffu, o[e], s);
@@ -104,7 +99,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
     }
     m = mn;
   }
-  const float inv = inverse_sum(lr);  // a row that sees no key: zeros
+  const float inv = inverse_sum(l);  // a row that sees no key: zeros
   const int t = (int)(row / a.Hq), hq = (int)(row - (long long)t * a.Hq);
   if (act && grp == 0) {
     uint4 r;

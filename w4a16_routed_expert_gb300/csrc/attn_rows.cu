@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               if (t4 == 0) {
                 if (!done)
-                  ln.part_ml[cur.prow + r] = make_float4(mt[m][e], lt[m][e], lt[m][e], 0.f);
+                  ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
                 else if (a.lse)
                   a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mt[m][e], lt[m][e]);
                 if (cur.parts) write_info(a, ln, cur, r, at);

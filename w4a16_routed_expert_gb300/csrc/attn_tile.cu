@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool done = whole(ln, *cur);
           const int2 at = cur->parts ? row_place(a, *cur, r) : make_int2(0, 0);
           const float l = l2.x + l2.y, lr = RSUM ? lr2.x + lr2.y : l, inv = inverse_sum(lr);
+          const float own = l == lr ? 1.f : l / lr;  // a partial stands against the sum l
           float* dst = ln.part_o + (long long)(cur->prow + r) * DP;
           T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D;
 #pragma unroll 1
@@ -571,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait_for(o);
             if (r < cur->rows) {
               if (!done) {
+                if (RSUM) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * own);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
               } else {
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (r < cur->rows) {
             if (!done)
-              ln.part_ml[cur->prow + r] = make_float4(mref, l, lr, 0.f);
+              ln.part_ml[cur->prow + r] = make_float2(mref, l);
             else if (a.lse)
               a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l);
             if (cur->parts) write_info(a, ln, *cur, r, at);
