@@ -101,22 +101,31 @@ inline long long line_places(const AttnArgs& a, const LineArgs& ln) {
 bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int page_size, int Hk, long long num_pages,
                       long long page_stride, long long slot_stride, long long head_stride, int slots, bool whole_head);
 
-// Few rows to a key (at most 32): legacy tensor-core tiles of 16 rows.
-constexpr int kRowsMax = 32;       // rows of a group it takes
+// Few rows to a key: tiles of 16 rows on mma.sync. Up to 32 rows at head sizes
+// to 64, up to 16 above: there two row tiles' outputs do not fit the registers
+// beside a second block (20 rows of 128 over 16 sequences of 8000 keys: 173 us,
+// 138 with one block an SM, 95 on the tcgen05 tiles; at 64, 20 rows behind 8192
+// keys: 23 us, 29 on the tcgen05 tiles).
+constexpr int kRowsMax = 32;
+constexpr int rows_most(int D) { return D <= 64 ? kRowsMax : 16; }
 constexpr int kRowsKeyTile = 64;
 struct AttnRowsPlan {
   int n_cta, stages;
   size_t smem;
 };
 AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms);
-constexpr int kRowsWeight = 2;   // LineArgs::weight
+// LineArgs::weight (0, 1, 2, 3, 5 for 16 sequences behind 4099 keys: 36.4, 26.1,
+// 26.0, 26.1, 26.9 us; for 48 sequences of drafts: 59.5, 50.5, 47.7, 48.1, 48.5)
+constexpr int kRowsWeight = 2;
 cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              const AttnRowsPlan& plan, int box_slots, bool bf16, bool late_wait, cudaStream_t s, bool pdl);
 
 // Many rows to a key: 128-row tcgen05 tiles, two to a block, one block per SM.
 constexpr int kTileRows = 256;
 constexpr int kTileKeyTile = 128;
-constexpr int kTileWeight = 3;   // LineArgs::weight
+// LineArgs::weight (0, 2, 3, 5, 8 for 48 sequences of drafts: 50.9, 48.5, 47.7,
+// 49.6, 49.3 us; for 64 behind 32768 keys: 88.1, 84.0, 83.6, 83.3, 83.5)
+constexpr int kTileWeight = 3;
 cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                              int box_slots, bool bf16, cudaStream_t s, bool pdl);
 

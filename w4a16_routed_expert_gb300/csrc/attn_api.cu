@@ -187,10 +187,11 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   const bool bf16 = h->cfg.dtype == MOE_DTYPE_BF16;
   const int own_rows = a.max_seq_len > 0 ? a.max_q_len * a.g : 0;
   const int prefix_rows = a.prefix_len > 0 ? (int)std::min<long long>((long long)a.T * a.g, INT_MAX / 2) : 0;
-  // Up to 32 rows to a key go to the few-row kernel (16-row tiles, no padding
-  // to speak of, two blocks an SM), more to the 128-row tiles of the tcgen05
+  // Few rows to a key go to the few-row kernel (16-row tiles, hardly any
+  // padding, two blocks an SM), more to the 128-row tiles of the tcgen05
   // kernel, of which a block takes two.
-  const bool tile_own = own_rows > moe::kRowsMax, tile_prefix = prefix_rows > moe::kRowsMax || (tile_own && prefix_rows);
+  const int most = moe::rows_most(a.D);
+  const bool tile_own = own_rows > most, tile_prefix = prefix_rows > most || (tile_own && prefix_rows);
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
   // Sequences of a row block and more on average: no block would serve two of
   // them, so the prefix is read in one go with the own keys (one partial

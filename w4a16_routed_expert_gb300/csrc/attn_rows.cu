@@ -1,12 +1,18 @@
 // Attention for few query rows to a key: a decode step over each sequence's
 // own pages, drafted tokens, or a prefix shared by a handful of rows.
 //
-// A group's rows (at most 32, in one or two tiles of 16) meet a run of its
-// keys: S = Q K^T, running softmax, O += P V, one pass over the keys. Every
-// key and value is read once by one block, so the bound is memory; what has
-// to hold is that the SM's copies never wait. Per SM at the measured 6.8 TB/s
-// a 16-key step (8 KB at head size 128) takes ~350 cycles; its 16-row tiles
-// cost ~120 issue slots, spread over the SM's eight computing warps.
+// A group's rows (at most 16, or 32 in two tiles at head sizes to 64) meet a
+// run of its keys: S = Q K^T, running softmax, O += P V, one pass over the
+// keys. Every key and value is read once by one block, so the bound is
+// memory; what has to hold is that the SM's copies never wait. Per SM at the
+// measured copy rate a 16-key step (8 KB at head size 128) takes ~350 cycles;
+// its 16-row tiles cost ~150 issue slots, spread over the SM's eight computing
+// warps. That leaves room to multiply the probabilities in two 16-bit parts.
+// Measured: 32 sequences of up to 24000 own keys, 8 key heads of 128 (1.53
+// GB), 230 us = 6.65 TB/s, 0.98 of the measured copy rate; 16 behind 4099
+// shared keys with up to 1000 own (92 MB) 26 us: 4 us until the first copy
+// (two dependent loads, then the page's number), 12 us of copies at full rate,
+// 1.5 us to end each part, 4 us for the join.
 //
 // A block is four computing warps and one that copies. Keys and values come
 // page by page as TMA boxes (16 to 64 slots of one head, 128-byte swizzle)
@@ -470,7 +476,9 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
     return launch_ex(kern, dim3(p.n_cta), dim3(kThreads), p.smem, s, pdl, tk, tv, a, ln, p.stages, box_log2,
                      (int)late_wait);
   };
-  return ln.part_rows <= 16 ? run(k_attn_rows<T, DP, 1>) : run(k_attn_rows<T, DP, 2>);
+  if constexpr (rows_most(DP) > 16)
+    if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2>);
+  return run(k_attn_rows<T, DP, 1>);
 }
 
 }  // namespace

@@ -10,6 +10,11 @@
 // peak for two row tiles) and 64 KB of keys and values (~2800 cycles at the
 // measured copy rate): up to ~190 rows the keys' bytes bound it, above that
 // the products.
+// Measured: four chunks of 301 to 1024 tokens behind 8200 keys, 32 query and 8
+// key heads of 128, 345 us = 1.37 PFLOP/s, 0.71 of the measured bf16 rate; a
+// key tile then takes 2700 to 2950 cycles. P V runs at the tensor cores' rate
+// (64 cycles an MMA), Q K^T, which reads both operands from shared memory, at
+// ~95; the softmax of a row tile takes 1000 to 1300 and hides.
 //
 // Warp roles (one block per SM):
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (a warp reaches the 32 lanes of
