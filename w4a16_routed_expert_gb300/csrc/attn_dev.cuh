@@ -35,26 +35,20 @@ struct Half16<__nv_bfloat16> {
   static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 };
 
-// Sequence b's query tokens, clamped to the batch: [*t0, *t0 + return).
-__device__ __forceinline__ int seq_tokens(const AttnArgs& a, int b, int* t0) {
-  const int lo = __ldg(a.q_offsets + b), hi = __ldg(a.q_offsets + b + 1);
-  const int n = hi - lo;
-  if (lo < 0 || hi > a.T || n < 0 || n > a.max_q_len) {
-    record_error(a.err, kAttnErrBounds);
-    *t0 = min(max(lo, 0), a.T);
-    return min(min(max(n, 0), a.max_q_len), a.T - *t0);
-  }
-  *t0 = lo;
-  return n;
-}
-// Sequence b's own keys, clamped to the bound the caller gave.
-__device__ __forceinline__ int seq_keys(const AttnArgs& a, int b) {
-  const int n = __ldg(a.seq_lens + b);
-  if (n < 0 || n > a.max_seq_len) {
-    record_error(a.err, kAttnErrBounds);
-    return min(max(n, 0), a.max_seq_len);
-  }
-  return n;
+// A sequence of the batch: its query tokens [t0, t0 + n) and its own keys,
+// clamped to the batch and to the bounds the caller gave. All three words are
+// asked for before any is looked at.
+struct Seq {
+  int t0, n, keys;
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  const int lo = __ldg(a.q_offsets + b), hi = __ldg(a.q_offsets + b + 1), keys = __ldg(a.seq_lens + b);
+  Seq s;
+  s.t0 = min(max(lo, 0), a.T);
+  s.n = min(min(max(hi - lo, 0), a.max_q_len), a.T - s.t0);
+  s.keys = min(max(keys, 0), a.max_seq_len);
+  if (s.t0 != lo || s.n != hi - lo || s.keys != keys) record_error(a.err, kAttnErrBounds);
+  return s;
 }
 // A page of the cache, clamped to it.
 __device__ __forceinline__ int page_in_cache(const AttnArgs& a, int page) {

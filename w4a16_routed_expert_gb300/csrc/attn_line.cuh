@@ -47,12 +47,11 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
   const int front = front_tiles<KT>(a, ln);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    int t0;
-    const int n = seq_tokens(a, b, &t0), keys = seq_keys(a, b);
-    const int blocks = row_blocks<RB>(a, n);
+    const Seq q = load_seq(a, b);
+    const int blocks = row_blocks<RB>(a, q.n);
     int span = 0;
 #pragma unroll 1
-    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of<KT>(block_keys<RB>(a, keys, n, rb)));
+    for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of<KT>(block_keys<RB>(a, q.keys, q.n, rb)));
     own_off[b + 1] = span;
     sum += span;
   }
@@ -105,10 +104,12 @@ struct Walk {
   int rb;
   Segment s;           // b, h, t0, n, klen, nkeys of the group
 
-  __device__ __forceinline__ void load_seq(const AttnArgs& a, int b) {
+  __device__ __forceinline__ void set_seq(const AttnArgs& a, int b) {
+    const Seq q = load_seq(a, b);
     s.b = b;
-    s.n = seq_tokens(a, b, &s.t0);
-    s.klen = seq_keys(a, b);
+    s.t0 = q.t0;
+    s.n = q.n;
+    s.klen = q.keys;
     blocks = row_blocks<RB>(a, s.n);
   }
   __device__ __forceinline__ void set_group(const AttnArgs& a, const LineArgs& ln) {
@@ -119,7 +120,7 @@ struct Walk {
   // The first group of own keys that has any, from sequence b on.
   __device__ __forceinline__ void first_own(const AttnArgs& a, const LineArgs& ln, const int32_t* own_off, int b) {
     while (b < a.B - 1 && own_off[b + 1] == own_off[b]) ++b;
-    load_seq(a, b);
+    set_seq(a, b);
     s.h = 0;
     rb = 0;
     set_group(a, ln);
@@ -172,7 +173,7 @@ struct Walk {
         hi = mid - 1;
     }
     const int per_head = max(1, own_off[lo + 1] - own_off[lo]);
-    load_seq(a, lo);
+    set_seq(a, lo);
     s.h = min((int)((y - (unsigned)own_off[lo] * a.Hk) / (unsigned)per_head), a.Hk - 1);
     start = total_prefix + own_off[lo] * a.Hk + s.h * per_head;
     rb = 0;

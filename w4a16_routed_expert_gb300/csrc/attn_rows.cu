@@ -82,6 +82,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (tid == kWarps * 32) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
   pdl_trigger();
   if (!late_wait) pdl_wait();
   const int own_total = scan_own<kThreads, kKT, MT * 16>(a, ln, own_off, scratch);
