@@ -229,6 +229,10 @@ FORWARD = {  # dtype, Hq, Hk, D, page, order, query lengths, own keys, prefix, c
     "short chunks behind a prefix": (F16, 8, 2, 64, 64, "slot", [20, 9, 33], [20, 70, 500], 600, True),
     "two thousand tokens": (F16, 2, 1, 64, 16, "slot", [2000], [2100], 130, True),
     "as many groups as there are keys": (BF16, 64, 64, 128, 16, "slot", [1] * 12, [i % 5 for i in range(12)], 0, True),
+    "a prefix of many rows beside own keys": (F16, 16, 4, 128, 16, "slot", [1] * 37, [(11 * i) % 90 for i in range(37)], 7301, True),
+    "the same in heads of 96": (BF16, 32, 4, 96, 48, "head", [1] * 19, [(7 * i) % 70 for i in range(19)], 7000, False),
+    "a prefix of many rows beside drafts": (BF16, 32, 8, 64, 32, "head", [(3 * i) % 6 for i in range(30)], [5 + (13 * i) % 100 for i in range(30)], 2000, True),
+    "a prefix of many rows alone": (F16, 16, 2, 128, 128, "slot", [1] * 40, [0] * 40, 700, True),
     "very unequal": (F16, 16, 4, 128, 32, "head", [1] * 9, [1, 4100, 2, 0, 3, 64, 65, 8, 700], 0, True),
 }
 

@@ -108,6 +108,13 @@ bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int 
 // keys: 23 us, 29 on the tcgen05 tiles).
 constexpr int kRowsMax = 32;
 constexpr int rows_most(int D) { return D <= 64 ? kRowsMax : 16; }
+// (query token, query head, prefix key) triples up to which it takes the
+// prefix's rows beside few own rows, however many. In its launch / in one of
+// the tcgen05 kernel before it, own keys to 200: 24 rows of 128 over 300, 4000,
+// 16000 prefix keys of 16 heads (0.1, 1.5, 6.1 million) 15 / 23, 24 / 31, 44 /
+// 48 us; 96 rows over 4000, 16000 of 8 heads (3.1, 12) 23 / 27, 54 / 38; 256
+// rows of 64 over 1000, 4000 (2.0, 8.2) 21 / 24, 33 / 27.
+constexpr long long kFewTriples = 1LL << 22;
 constexpr int kRowsKeyTile = 64;
 struct AttnRowsPlan {
   int n_cta, stages;

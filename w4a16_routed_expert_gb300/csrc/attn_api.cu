@@ -189,9 +189,13 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   const int prefix_rows = a.prefix_len > 0 ? (int)std::min<long long>((long long)a.T * a.g, INT_MAX / 2) : 0;
   // Few rows to a key go to the few-row kernel (16-row tiles, hardly any
   // padding, two blocks an SM), more to the 128-row tiles of the tcgen05
-  // kernel, of which a block takes two.
+  // kernel, of which a block takes two. Beside few own rows a prefix of many
+  // stays in the few-row kernel's launch while there is little to compute, in
+  // row blocks that read its keys once each.
   const int most = moe::rows_most(a.D);
-  const bool tile_own = own_rows > most, tile_prefix = prefix_rows > most || (tile_own && prefix_rows);
+  const bool little = own_rows && (long long)a.T * a.Hq * a.prefix_len <= moe::kFewTriples;
+  const bool tile_own = own_rows > most;
+  const bool tile_prefix = prefix_rows && (tile_own || (prefix_rows > most && !little));
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
   // Sequences of a row block and more on average: no block would serve two of
   // them, so the prefix is read in one go with the own keys (one partial
@@ -234,8 +238,9 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
     fits = line(&tile, moe::kTileRows, moe::kTileKeyTile, moe::kTileWeight, h->num_sms, tile_prefix, tile_own);
   if (few_own || few_prefix) {
     const int rows = std::max(few_own ? own_rows : 0, few_prefix ? prefix_rows : 0);
-    plan = moe::plan_attn_rows(a.D, rows, a.B, h->num_sms);
-    fits = line(&few, rows <= 16 ? 16 : moe::kRowsMax, moe::kRowsKeyTile, moe::kRowsWeight, plan.n_cta, few_prefix,
+    const int block = rows <= 16 ? 16 : most;
+    plan = moe::plan_attn_rows(a.D, std::min(rows, block), a.B, h->num_sms);
+    fits = line(&few, block, moe::kRowsKeyTile, moe::kRowsWeight, plan.n_cta, few_prefix,
                 few_own) && fits;
   }
   if (!fits) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens and lengths beyond what one call takes", fn);
