@@ -233,6 +233,11 @@ FORWARD = {  # dtype, Hq, Hk, D, page, order, query lengths, own keys, prefix, c
     "the same in heads of 96": (BF16, 32, 4, 96, 48, "head", [1] * 19, [(7 * i) % 70 for i in range(19)], 7000, False),
     "a prefix of many rows beside drafts": (BF16, 32, 8, 64, 32, "head", [(3 * i) % 6 for i in range(30)], [5 + (13 * i) % 100 for i in range(30)], 2000, True),
     "a prefix of many rows alone": (F16, 16, 2, 128, 128, "slot", [1] * 40, [0] * 40, 700, True),
+    "83 tokens after 8940 keys": (F16, 16, 16, 64, 16, "slot", [83], [8940], 0, True),
+    "80 tokens of three heads after 9000 keys": (BF16, 48, 16, 64, 64, "head", [80], [9000], 0, True),
+    "83 tokens of 128 after 6000 keys": (BF16, 16, 16, 128, 16, "slot", [83], [6000], 0, True),
+    "80 tokens of three heads of 128 after 7000 keys": (F16, 48, 16, 128, 32, "slot", [80], [7000], 0, True),
+    "a long prefix and 70 tokens each": (F16, 16, 16, 64, 16, "head", [70, 70], [90, 1200], 6000, True),
     "very unequal": (F16, 16, 4, 128, 32, "head", [1] * 9, [1, 4100, 2, 0, 3, 64, 65, 8, 700], 0, True),
 }
 
@@ -271,6 +276,28 @@ def test_logits_that_grow_or_fall_along_the_keys(rows, slope):
         want, wlse, tol, ltol = AO.attend(q, ks, vs, q_lens, 401, own, D ** -0.5, True)
         within(out, want, tol, "out")
         within(lse, wlse, ltol, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens,g", [(1, 8), (90, 1), (70, 3)])
+def test_logits_that_move_over_many_tiles(D, tokens, g):
+    """Each block takes many tiles in a row and moves its reference again and
+    again: up, then down, then up by jumps past what FP16 weights can hold."""
+
+    def keys(Hk, n, D, gen):
+        k = torch.randn(Hk, n, D, generator=gen) * 0.3
+        x = torch.linspace(0, 1, n)
+        k[:, :, 0] += 30 * torch.sin(9 * x)[None] + 12 * (torch.arange(n) % 1500 == 700)[None]
+        return k
+
+    Hk, n = 16, 7000
+    a, q, ks, vs, args = build(F16, Hk * g, Hk, D, 32, "slot", [tokens], [n], 0, seed=7, keys=keys)
+    q[..., 0] = 5.0
+    out, lse = a.forward(q.cuda(), return_lse=True, **args)
+    a.sync()
+    want, wlse, tol, ltol = AO.attend(q, ks, vs, [tokens], 0, [n], D ** -0.5, True)
+    within(out, want, tol, "out")
+    within(lse, wlse, ltol, "lse")
 
 
 @pytest.mark.parametrize("rows", ["few", "many"])

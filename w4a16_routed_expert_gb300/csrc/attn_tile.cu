@@ -31,13 +31,13 @@
 //                   probabilities' barrier: a wait costs ~170 cycles even when
 //                   it is complete, and the tensor cores hold only a few MMAs
 //                   in advance, so the MMA warp waits once a row tile
-// Tensor memory: two S tiles (P takes the first half of S's columns) and two
-// output tiles, 512 columns at head size 128.
+// Tensor memory: two S tiles (three at head sizes to 64; P takes the first half
+// of S's columns) and two output tiles, 512 columns.
 //
-// MMAs of one lane run in order, so Q K^T of the next tile may overwrite
-// the columns that the P V issued just before it reads; and a completed
-// Q K^T means the P V before it has completed, so the softmax warps may
-// rescale the output without another barrier.
+// MMAs of one lane run in order, so a Q K^T may overwrite the columns that the
+// P V issued before it reads. At head sizes above 64 a completed Q K^T means
+// that the P V before it has completed, so the softmax warps may rescale the
+// output without another barrier; below, with three S tiles, they wait for it.
 #include "attn_line.cuh"
 #include "attn_tc.cuh"
 
@@ -59,7 +59,7 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
   SmemPlan p;
   p.ring = 2u * 128 * DP * 2;  // after the queries
   p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
-  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 10) * 8;
+  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 16) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 80;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
@@ -85,16 +85,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   constexpr int NH = DP / 64;
   constexpr bool kBf16 = sizeof(T) == 2 && ProbBias<T>::value == 0.f;
+  // Head sizes to 64 leave room for a third S tile: the next key tile's Q K^T is
+  // issued before a row tile's probabilities are in, S_t(j) in place (2 j + t)
+  // mod 3, which the P V two before it has left (four chunks of 770 tokens, 32
+  // query heads of 64: 280 us, 313 with two S tiles).
+  constexpr bool kAhead = DP == 64;
+  constexpr uint32_t kOut = kAhead ? 384 : 256;     // columns of the output tiles
   constexpr uint32_t kHalf = 128 * 128;             // bytes of 64 elements of 128 rows
   constexpr uint32_t kTileBytes = NH * kHalf;       // a query, key or value tile
   const SmemPlan sp = smem_plan(DP, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
   uint64_t* q_full = empty + kMaxStages;  // [2] queries in shared memory and the output tile drained
-  uint64_t* s_full = q_full + 2;          // [2] logits in tensor memory
-  uint64_t* p_full = s_full + 2;          // [2] probabilities in tensor memory
-  uint64_t* o_full = p_full + 2;          // [2] output complete
-  uint64_t* seg_full = o_full + 2;
+  // [2][2] by row tile and, with kAhead, by the key tile's parity: those of two
+  // tiles in a row may be complete before the other side has looked, and a
+  // phase two ahead would look like the one before it
+  uint64_t* s_full = q_full + 2;          // logits in tensor memory
+  uint64_t* p_full = s_full + 4;          // probabilities in tensor memory
+  uint64_t* o_full = p_full + 4;          // output complete (kAhead: with each key tile)
+  uint64_t* seg_full = o_full + 4;
   uint64_t* seg_empty = seg_full + kSegSlots;
   uint64_t* drain = seg_empty + kSegSlots;
   Segment* segs = reinterpret_cast<Segment*>(smem + sp.seg);
@@ -110,9 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 4);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 5);  // four softmax warps, kWarpLanded
-      mbar_init(&o_full[t], 1);
+      for (int par = 0; par < 2; ++par) {
+        mbar_init(&s_full[2 * t + par], 1);
+        mbar_init(&p_full[2 * t + par], 5);  // four softmax warps, kWarpLanded
+        mbar_init(&o_full[2 * t + par], 1);
+      }
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&seg_full[i], 1);
@@ -182,24 +193,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot = key - pg * a.page_size;
         return page_in_cache(a, __ldg((pre ? a.prefix_pages : own) + pg));
       };
+      auto issue = [&](const CUtensorMap* tm, int page, int at, int boxes) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
+        __syncwarp();
+        if (page >= 0) tma_load_5d(dst0 + (uint32_t)st * kTileBytes, tm, cx, at, ch, s.h, page, &full[st]);
+        ++issued;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      // keys and values in turn, with kAhead the next tile's keys before a
+      // tile's values: the order in which the MMA warp comes to them
       int page = page_of(s.tile);
+      int vpage = -1, vat = 0, vboxes = 0;
 #pragma unroll 1
-      for (int i = 0; i < s.tiles && ok; ++i) {
+      for (int i = 0; i < s.tiles + (kAhead ? 1 : 0) && ok; ++i) {
         const int at = slot, boxes = (here + box - 1) >> box_log2;
         const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : -1;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
-          __syncwarp();
-          if (page >= 0)
-            tma_load_5d(dst0 + (uint32_t)st * kTileBytes, kv ? &tv : &tk, cx, at, ch, s.h, page, &full[st]);
-          ++issued;
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1u;
-          }
+        if (i < s.tiles) issue(&tk, page, at, boxes);
+        if (!kAhead) {
+          if (ok) issue(&tv, page, at, boxes);
+        } else {
+          if (ok && i > 0) issue(&tv, vpage, vat, vboxes);
+          vpage = page;
+          vat = at;
+          vboxes = boxes;
         }
         page = next;
       }
@@ -216,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk = smem_desc_sw128(smem_u32(smem) + sp.ring);
       const uint64_t dv = smem_desc_rows_k(smem_u32(smem) + sp.ring, kHalf);
       int st = 0, slot_i = 0;
-      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, sph = 0;
+      uint32_t ph = 0, qph[2] = {0, 0}, pph[4] = {0, 0, 0, 0}, sph = 0;
       const uint32_t elect = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -228,14 +249,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1u;
         }
       };
-      auto qk = [&](int t, int stage) {
+      auto place = [&](int t, int j) { return (uint32_t)(kAhead ? (2 * j + t) % 3 : t) * 128; };
+      auto bar = [&](int t, int j) { return 2 * t + (kAhead ? j & 1 : 0); };
+      auto qk = [&](int t, int j, int stage) {
         const uint64_t q = dq + (uint64_t)(t * (kTileBytes >> 4)), k0 = dk + (uint64_t)(stage * (kTileBytes >> 4));
+        const uint32_t d = tm + place(t, j);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint64_t off = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
-          mma_ss(elect, tm + t * 128, q + off, k0 + off, id_s, k > 0);
+          mma_ss(elect, d, q + off, k0 + off, id_s, k > 0);
         }
-        commit_elect(elect, &s_full[t]);
+        commit_elect(elect, &s_full[bar(t, j)]);
+      };
+      // waits for the probabilities of (t, j) in tensor memory, and with them
+      // (kWarpLanded) for what the products up to the next wait read
+      auto pv = [&](int t, int j, int stage) {
+        const int i = bar(t, j);
+        if (!wait(&p_full[i], pph[i])) return false;
+        pph[i] ^= 1u;
+        tc_fence_after();
+        const uint64_t v0 = dv + (uint64_t)(stage * (kTileBytes >> 4));
+        const uint32_t d = tm + kOut + t * DP, p = tm + place(t, j);
+#pragma unroll
+        for (int k = 0; k < kKT / 16; ++k)
+          mma_ts(elect, d, p + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o, (j > 0 || k > 0) ? 1u : 0u);
+        return true;
       };
       bool ok = true;
       while (ok) {
@@ -257,38 +295,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           qph[t] ^= 1u;
           if (!ok) break;
           tc_fence_after();
-          qk(t, st);
+          qk(t, 0, st);
         }
         if (!ok) break;
         commit_elect(elect, &empty[st]);
         step();
+        if (!kAhead) {
 #pragma unroll 1
-        for (int i = 0; i < tiles && ok; ++i) {
-          const int vst = st;
-          const bool more = i + 1 < tiles;
-          step();
-          const uint64_t v0 = dv + (uint64_t)(vst * (kTileBytes >> 4));
+          for (int i = 0; i < tiles && ok; ++i) {
+            const int vst = st;
+            const bool more = i + 1 < tiles;
+            step();
 #pragma unroll 1
-          for (int t = 0; t < nt; ++t) {
-            // probabilities in tensor memory, this tile's values and the next
-            // one's keys in shared memory
-            ok = wait(&p_full[t], pph[t]);
-            pph[t] ^= 1u;
+            for (int t = 0; t < nt; ++t) {
+              ok = pv(t, i, vst);
+              if (!ok) break;
+              if (t == nt - 1) commit_elect(elect, &empty[vst]);
+              if (more)
+                qk(t, i + 1, st);
+              else
+                commit_elect(elect, &o_full[2 * t]);
+            }
+            if (ok && more) {
+              commit_elect(elect, &empty[st]);
+              step();
+            }
+          }
+        } else {
+          int k1 = st;  // stage of the next key tile
+          if (tiles > 1) {
+            ok = wait(&full[st], ph);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kKT / 16; ++k)
-              mma_ts(elect, tm + 256 + t * DP, tm + t * 128 + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o,
-                     (i > 0 || k > 0) ? 1u : 0u);
-            if (t == nt - 1) commit_elect(elect, &empty[vst]);
-            if (more)
-              qk(t, st);
-            else
-              commit_elect(elect, &o_full[t]);
-          }
-          if (ok && more) {
-            commit_elect(elect, &empty[st]);
+            qk(0, 1, k1);
+            if (nt == 1) commit_elect(elect, &empty[k1]);
             step();
+          }
+#pragma unroll 1
+          for (int i = 0; i < tiles; ++i) {
+            const int vst = st;
+            step();
+            const int k2 = st;  // of the one after it
+            if (i + 2 < tiles) step();
+            ok = pv(0, i, vst);
+            if (!ok) break;
+            commit_elect(elect, &o_full[bar(0, i)]);
+            if (nt == 2) {
+              if (i + 1 < tiles) {
+                qk(1, i + 1, k1);
+                commit_elect(elect, &empty[k1]);
+              }
+              ok = pv(1, i, vst);
+              if (!ok) break;
+              commit_elect(elect, &o_full[bar(1, i)]);
+            }
+            commit_elect(elect, &empty[vst]);
+            if (i + 2 < tiles) {
+              qk(0, i + 2, k2);
+              if (nt == 1) commit_elect(elect, &empty[k2]);
+            }
+            k1 = k2;
           }
         }
       }
@@ -296,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpLanded) {
     // -------------------------------------------------------------- landed
     int st = 0, slot_i = 0;
-    uint32_t ph = 0, sph = 0, pph[2] = {1, 1};  // p_full: parity of the phase before the one to join
+    uint32_t ph = 0, sph = 0, pph[4] = {1, 1, 1, 1};  // p_full: parity of the phase before the one to join
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)) != 0;
     };
@@ -320,14 +386,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
       }
       if (tiles == 0) break;
-      ok = landed();
+      auto join = [&](int t, int j) {
+        const int i = 2 * t + (kAhead ? j & 1 : 0);
+        if (!wait(&p_full[i], pph[i])) return false;  // the phase before is over: this arrival counts for the next
+        pph[i] ^= 1u;
+        if (lane == 0) mbar_arrive(&p_full[i]);
+        return true;
+      };
+      // behind P V of (t, i) the MMA warp goes on to the Q K^T of (t, i + 1), or
+      // with kAhead of the other row tile's next key tile
+      ok = landed() && (!kAhead || tiles == 1 || landed());
 #pragma unroll 1
       for (int i = 0; i < tiles && ok; ++i) {
-        ok = landed() && (i + 1 == tiles || landed());
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = wait(&p_full[t], pph[t]);  // the phase before is over: this arrival counts for the next
-          pph[t] ^= 1u;
-          if (ok && lane == 0) mbar_arrive(&p_full[t]);
+        if (!kAhead) {
+          ok = landed() && (i + 1 == tiles || landed());
+          for (int t = 0; t < nt && ok; ++t) ok = join(t, i);
+        } else {
+          ok = landed();
+          if (ok && nt == 2) ok = join(0, i);
+          if (ok && i + 2 < tiles) ok = landed();
+          if (ok) ok = join(nt - 1, i);
         }
       }
     }
@@ -337,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2;                       // row tile
     const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the group
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * DP;
+    const uint32_t to = tmem + lanes + kOut + t * DP;
     const float sc = a.scale * 1.44269504088896340736f;
     const float2 sc2 = make_float2(sc, sc);
     // queries of this row tile, 16 bytes a thread, consecutive threads along a
@@ -370,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    uint32_t sph = 0, oph = 0, gph = 0;
+    uint32_t sph[2] = {0, 0}, outs[2] = {0, 0}, gph = 0;  // outs: phases of o_full before this part
     int slot_i = 0;
     int vst = 0;  // ring stage of the next key tile, and its phase
     uint32_t vph = 0;
@@ -422,8 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool pre = tile0 + i < front;  // a tile of the prefix before own keys
           const int k0 = (tile0 + i - (pre ? 0 : front)) * kKT;
           const int nk = pre ? a.prefix_len : nkeys;
-          const bool got = mbar_wait(&s_full[t], sph, abort_flag, a.err);
-          sph ^= 1u;
+          const int par = kAhead ? i & 1 : 0;
+          const uint32_t ts = tmem + lanes + (uint32_t)(kAhead ? (2 * i + t) % 3 : t) * 128;
+          const bool got = mbar_wait(&s_full[2 * t + par], sph[par], abort_flag, a.err);
+          sph[par] ^= 1u;
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
@@ -478,6 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lr2.x *= f;
                 lr2.y *= f;
                 if (i > 0) {
+                  if (kAhead) {  // the P V before has been issued, but need not be over
+                    const int j = i - 1;
+                    mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
+                    __syncwarp();
+                    tc_fence_after();
+                  }
 #pragma unroll 1
                   for (int c = 0; c < DP / 32; ++c) {
                     uint32_t v[32];
@@ -487,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
                     tmem_st32(to + c * 32, v);
                   }
+                  tmem_st_wait();
                 }
               }
               const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
@@ -523,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (nk - k0 < kKT) {
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN)
-            int z = 2 * i + 1 + vst;  // the tile's values' place in the ring
+            // the tile's values' place in the ring
+            int z = 2 * i + (kAhead && i + 1 < tiles ? 2 : 1) + vst;
             const uint32_t zph = vph ^ ((uint32_t)(z / stages) & 1u);
             z %= stages;
             const bool there = mbar_wait(&full[z], zph, abort_flag, a.err);
@@ -541,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async_smem();
           }
           tc_fence_before();
-          arrive(&p_full[t]);
+          arrive(&p_full[2 * t + par]);
         }
       }
       if (!ok) break;
@@ -556,8 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more_used) load_q(&segs[slot_i]);
       }
       if (used) {
-        const bool got = mbar_wait(&o_full[t], oph, abort_flag, a.err);
-        oph ^= 1u;
+        const int j = kAhead ? tiles - 1 : 0;
+        const bool got = mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
+        outs[0] += (uint32_t)(j >> 1) + 1u;  // tiles 0, 2, ... and 1, 3, ...
+        outs[1] += (uint32_t)(j + 1) >> 1;
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
