@@ -132,7 +132,8 @@ typedef struct {
   const int32_t* q_offsets;    /* device [B + 1], ascending from 0 to T: sequence b's tokens */
   int32_t max_q_len;           /* at least every sequence's number of query tokens */
   const int32_t* seq_lens;     /* device [B]: sequence b's own keys (its query tokens' among them), 0 or more */
-  int32_t max_seq_len;         /* at least every seq_lens[b], at most table_stride * page_size */
+  int32_t max_seq_len;         /* at least every seq_lens[b], at most table_stride * page_size; 0: there are no own
+                                  keys, and seq_lens and q_offsets are not looked at */
   const int32_t* block_table;  /* device [B][table_stride]: own key j is in slot j % page_size of page
                                   block_table[b][j / page_size]; NULL when max_seq_len is 0 */
   int32_t table_stride;

@@ -75,7 +75,9 @@ def test_create_refuses(lib, bad, status):
 def test_create_refuses_pointers(lib):
     h = ctypes.c_void_p()
     for buf in (capi.moe_attn_buffers_t(k_cache=4096), capi.moe_attn_buffers_t(v_cache=4096),
-                capi.moe_attn_buffers_t(k_cache=4096, v_cache=8200)):
+                capi.moe_attn_buffers_t(k_cache=4096, v_cache=8200),
+                capi.moe_attn_buffers_t(k_cache=4096, v_cache=8192, q_norm=4100),
+                capi.moe_attn_buffers_t(k_norm=4104)):
         assert lib.moe_attn_create(ctypes.byref(config()), ctypes.byref(buf), ctypes.byref(h)) == capi.MOE_ERR_INVALID_ARG
     assert lib.moe_attn_create(None, None, ctypes.byref(h)) == capi.MOE_ERR_INVALID_ARG
     assert lib.moe_attn_create(ctypes.byref(config()), ctypes.byref(capi.moe_attn_buffers_t()), None) == capi.MOE_ERR_INVALID_ARG

@@ -516,7 +516,13 @@ moe_status_t moe_attn_sync(moe_attn_t* h, void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   uint32_t err = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&err, h->err, 4, cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && err) e = cudaMemset(h->err, 0, 4);
+  if (e == cudaSuccess && err) {
+    e = cudaMemset(h->err, 0, 4);
+    // a forward that gave up may have left words that its join did not read
+    const size_t words = (size_t)h->cfg.max_tokens * h->cfg.num_q_heads * sizeof(int2);
+    for (int i = 0; i < 2 && h->info[i] && e == cudaSuccess; ++i) e = cudaMemset(h->info[i], 0, words);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  }
   if (e != cudaSuccess) return cuda_error(e, fn);
   if (err == moe::kAttnErrTimeout) return set_error(MOE_ERR_TIMEOUT, "%s: a device-side wait gave up", fn);
   if (err) return set_error(MOE_ERR_INVALID_ARG, "%s: a slot, page, length or offset was out of range", fn);
