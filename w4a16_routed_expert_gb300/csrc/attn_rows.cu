@@ -108,7 +108,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     while (ok) {
       Segment s;
       const bool some = w.next(a, ln, own_off, &s);
-      if (!some) s.tiles = 0;
+      if (!some) {
+        s.tiles = 0;
+        s.tile = s.b = s.nkeys = s.front = 0;  // no page to ask for
+      }
+      const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      int slot = 0;  // of the page, of the lane's box of the current tile
+      bool have = false;  // that box has keys
+      auto page_of = [&](int tile) {
+        const int key = tile * kKT + (c << box_log2);
+        have = mine && key < s.nkeys;
+        if (!have) return 0;
+        const int pg = key / a.page_size;
+        slot = key - pg * a.page_size;
+        return __ldg(tab + pg);  // looked at (page_in_cache) when it is used, not before
+      };
+      int page = page_of(s.tile);
+      // (the first page's number is on its way meanwhile)
       ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
       if (!ok) break;
       if (lane == 0) {
@@ -120,26 +136,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         sph ^= 1u;
       }
       if (!some) break;
-      const int32_t* tab = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
-      int slot = 0;  // of the page, of the lane's box of the current tile
-      auto page_of = [&](int tile) {
-        const int key = tile * kKT + (c << box_log2);
-        if (!mine || key >= s.nkeys) return -1;
-        const int pg = key / a.page_size;
-        slot = key - pg * a.page_size;
-        return page_in_cache(a, __ldg(tab + pg));
-      };
-      int page = page_of(s.tile);
 #pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
         const int tile = s.tile + i, at = slot;
-        const int next = i + 1 < s.tiles ? page_of(tile + 1) : -1;
+        const bool has = have;
+        const int next = i + 1 < s.tiles ? page_of(tile + 1) : 0;
         const int boxes = (min(kKT, max(0, s.nkeys - tile * kKT)) + box - 1) >> box_log2;
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * 2 * box * DP * 2);
         __syncwarp();
-        if (page >= 0) {
+        if (has) {
+          page = page_in_cache(a, page);
           const uint32_t dst = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes + (lane < 16 ? 0u : kTileBytes) +
                                (uint32_t)c * box * DP * 2;
           if (split) {

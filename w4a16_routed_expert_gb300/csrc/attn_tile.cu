@@ -168,7 +168,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok) {
       Segment s;
       const bool some = w.next(a, ln, own_off, &s);
-      if (!some) s.tiles = 0;
+      if (!some) {
+        s.tiles = 0;
+        s.tile = s.b = s.nkeys = s.front = 0;  // no page to ask for
+      }
+      const int32_t* own = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
+      int slot = 0;  // of the page, of the lane's box of the current tile
+      int here = 0;  // keys of the tile that exist
+      bool have = false;  // the lane's box has any
+      auto page_of = [&](int tile) {
+        const bool pre = tile < s.front;
+        const int k0 = (pre ? tile : tile - s.front) * kKT, key = k0 + (c << box_log2);
+        const int nk = pre ? a.prefix_len : s.nkeys;
+        here = min(kKT, max(0, nk - k0));
+        have = mine && key < nk;
+        if (!have) return 0;
+        const int pg = key / a.page_size;
+        slot = key - pg * a.page_size;
+        return __ldg((pre ? a.prefix_pages : own) + pg);  // looked at (page_in_cache) when it is used, not before
+      };
+      auto issue = [&](const CUtensorMap* tm, bool some_keys, int page, int at, int boxes) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
+        __syncwarp();
+        if (some_keys)
+          tma_load_5d(dst0 + (uint32_t)st * kTileBytes, tm, cx, at, ch, s.h, page_in_cache(a, page), &full[st]);
+        ++issued;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      // keys and values in turn, with kAhead the next tile's keys before a
+      // tile's values: the order in which the MMA warp comes to them
+      int page = page_of(s.tile);
+      // (the first page's number is on its way meanwhile)
       ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
       if (!ok) break;
       if (lane == 0) {
@@ -180,44 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
       }
       if (!some) break;
-      const int32_t* own = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
-      int slot = 0;  // of the page, of the lane's box of the current tile
-      int here = 0;  // keys of the tile that exist
-      auto page_of = [&](int tile) {
-        const bool pre = tile < s.front;
-        const int k0 = (pre ? tile : tile - s.front) * kKT, key = k0 + (c << box_log2);
-        const int nk = pre ? a.prefix_len : s.nkeys;
-        here = min(kKT, max(0, nk - k0));
-        if (!mine || key >= nk) return -1;
-        const int pg = key / a.page_size;
-        slot = key - pg * a.page_size;
-        return page_in_cache(a, __ldg((pre ? a.prefix_pages : own) + pg));
-      };
-      auto issue = [&](const CUtensorMap* tm, int page, int at, int boxes) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
-        __syncwarp();
-        if (page >= 0) tma_load_5d(dst0 + (uint32_t)st * kTileBytes, tm, cx, at, ch, s.h, page, &full[st]);
-        ++issued;
-        if (++st == stages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      };
-      // keys and values in turn, with kAhead the next tile's keys before a
-      // tile's values: the order in which the MMA warp comes to them
-      int page = page_of(s.tile);
-      int vpage = -1, vat = 0, vboxes = 0;
+      int vpage = 0, vat = 0, vboxes = 0;
+      bool vhave = false;
 #pragma unroll 1
       for (int i = 0; i < s.tiles + (kAhead ? 1 : 0) && ok; ++i) {
         const int at = slot, boxes = (here + box - 1) >> box_log2;
-        const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : -1;
-        if (i < s.tiles) issue(&tk, page, at, boxes);
+        const bool has = have;
+        const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : 0;
+        if (i < s.tiles) issue(&tk, has, page, at, boxes);
         if (!kAhead) {
-          if (ok) issue(&tv, page, at, boxes);
+          if (ok) issue(&tv, has, page, at, boxes);
         } else {
-          if (ok && i > 0) issue(&tv, vpage, vat, vboxes);
+          if (ok && i > 0) issue(&tv, vhave, vpage, vat, vboxes);
+          vhave = has;
           vpage = page;
           vat = at;
           vboxes = boxes;
