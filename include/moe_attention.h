@@ -26,7 +26,9 @@
  * Types: queries, keys, values, outputs and the cache are all FP16 or all
  * BF16; norms, angles, logits, softmax statistics and sums are FP32. Results
  * are rounded once when they are stored. (The probabilities that multiply
- * the values are rounded to the 16-bit type first, for the tensor cores.)
+ * the values go to the tensor cores in the 16-bit type: in two parts, which
+ * lose nothing beside the result's own rounding, where few rows read a key,
+ * in one otherwise.)
  *
  * Conventions are those of moe_layer.h: every call returns a moe_status_t
  * (moe_layer_last_error(NULL) describes the calling thread's last failure),
