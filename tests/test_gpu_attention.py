@@ -238,6 +238,9 @@ FORWARD = {  # dtype, Hq, Hk, D, page, order, query lengths, own keys, prefix, c
     "83 tokens of 128 after 6000 keys": (BF16, 16, 16, 128, 16, "slot", [83], [6000], 0, True),
     "80 tokens of three heads of 128 after 7000 keys": (F16, 48, 16, 128, 32, "slot", [80], [7000], 0, True),
     "a long prefix and 70 tokens each": (F16, 16, 16, 64, 16, "head", [70, 70], [90, 1200], 6000, True),
+    "three thousand sequences": (F16, 2, 1, 64, 16, "slot", [1] * 3000, [(7 * i) % 40 for i in range(3000)], 50, True),
+    "three thousand behind a long prefix": (BF16, 1, 1, 128, 16, "slot", [1] * 3000, [(5 * i) % 20 for i in range(3000)], 1500, True),
+    "the most sequences": (F16, 1, 1, 8, 16, "head", [1] * 4096, [(3 * i) % 35 for i in range(4096)], 0, True),
     "very unequal": (F16, 16, 4, 128, 32, "head", [1] * 9, [1, 4100, 2, 0, 3, 64, 65, 8, 700], 0, True),
 }
 
