@@ -77,7 +77,7 @@ struct LineArgs {
   int part_rows;         // rows a partial takes at most: min(row_block, most rows of a group)
   int part_row0;         // this kernel's first row of partials
   float* part_o;         // [rows][DP]: block c's partial of a group stands at the group's first row + c * part_rows
-  float2* part_ml;       // [rows] maximum (log2 units), sum
+  float2* part_ml;       // [rows] reference maximum (a logit before the scale), sum
   int2 *info_prefix, *info_own;  // [T][Hq] first partial row and number of partials, 0 between forwards
   int final_prefix, final_own;   // 1: these groups' rows have no other partials, one part alone is the result
 };

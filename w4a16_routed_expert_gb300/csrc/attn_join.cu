@@ -1,8 +1,8 @@
 // Joins the partial results of one forward: for each (query token, query
-// head) the rows that the blocks left in the workspace (maximum m_i in powers
-// of two, sum l_i, output o_i relative to 2^m_i) become
-//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i,
-//   lse = ln 2 (m + log2 sum_i 2^(m_i - m) l_i) - ln 2 * bias
+// head) the rows that the blocks left in the workspace (reference logit m_i,
+// sum l_i and output o_i of weights taken against it) become
+//   out = sum_i w_i o_i / sum_i w_i l_i,  w_i = e^(scale (m_i - m)),  m = max_i m_i,
+//   lse = scale m + ln sum_i w_i l_i - ln 2 * bias
 // in a fixed order. The partials were just written, so the reads mostly hit
 // L2; what bounds it is the chain of two loads (where the partials are, then
 // they) of the rows in flight.
@@ -42,8 +42,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
   const bool act = gl * 8 < a.D;
   float m = -INFINITY, l = 0.f;
   float o[8] = {};
+  const float sc = a.scale * kLog2e;
   // m and the running sums move to max(m, mi); -inf stays -inf
-  auto scale_to = [&](float mn, float mi) { return mi == mn ? 1.f : exp2_fast(mi - mn); };
+  auto scale_to = [&](float mn, float mi) { return mi == mn ? 1.f : exp2_fast((mi - mn) * sc); };
 #pragma unroll 1
   for (int i = grp; i < n; i += G * U) {
     float2 v[U];
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
     r.w = Half16<T>::pack(o[6] * inv, o[7] * inv);
     *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)t * a.out_stride + (long long)hq * a.D + gl * 8) = r;
   }
-  if (a.lse && lane == 0) a.lse[row] = log_sum<T>(m, l);
+  if (a.lse && lane == 0) a.lse[row] = log_sum<T>(m, l, a.scale);
 }
 
 template <typename T>

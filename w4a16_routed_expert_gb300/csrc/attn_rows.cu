@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     // ------------------------------------------------------------ compute
     const int g8 = lane >> 2, t4 = lane & 3;
-    const float sc = a.scale * 1.44269504088896340736f;  // logits in powers of two
+    const float sc = a.scale * kLog2e;
     // shared-memory address parts of this warp's 16 keys (all in one box)
     const uint32_t warp_off = (uint32_t)((warp * 16) >> box_log2) * box * DP * 2 + (uint32_t)((warp * 16) & (box - 1)) * 128;
     const uint32_t half_step = (uint32_t)box * 128;
@@ -307,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 2; ++e) {
               mx[e] = fmaxf(fmaxf(sv[m][0][2 * e], sv[m][0][2 * e + 1]), fmaxf(sv[m][1][2 * e], sv[m][1][2 * e + 1]));
               mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * sc;
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
             }
-            if (__any_sync(0xffffffffu, mx[0] > mref[m][0] + kLazy || mx[1] > mref[m][1] + kLazy)) {
+            if (__any_sync(0xffffffffu, (mx[0] - mref[m][0]) * sc > kLazy || (mx[1] - mref[m][1]) * sc > kLazy)) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float mn = fmaxf(mref[m][e], mx[e]);
-                const float f = mref[m][e] == mn ? 1.f : exp2_fast(mref[m][e] - mn);
+                const float f = mref[m][e] == mn ? 1.f : exp2_fast((mref[m][e] - mn) * sc);
                 mref[m][e] = mn;
                 l[m][e] *= f;
 #pragma unroll
@@ -326,14 +326,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             float p[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float ref = (mref[m][e] == -INFINITY ? 0.f : mref[m][e]) - ProbBias<T>::value;
+              const float ref = mref[m][e] == -INFINITY ? 0.f : mref[m][e];
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  p[n][2 * e + f] = exp2_fast(fmaf(sv[m][n][2 * e + f], sc, -ref));
-                  l[m][e] += p[n][2 * e + f];
-                }
+              for (int n = 0; n < 2; ++n) {
+                float2 w = fadd2(make_float2(sv[m][n][2 * e], sv[m][n][2 * e + 1]), make_float2(-ref, -ref));
+                w = ffma2(w, make_float2(sc, sc), make_float2(ProbBias<T>::value, ProbBias<T>::value));
+                p[n][2 * e] = exp2_fast(w.x);
+                p[n][2 * e + 1] = exp2_fast(w.y);
+                l[m][e] += p[n][2 * e];
+                l[m][e] += p[n][2 * e + 1];
+              }
             }
             // the weights as two 16-bit numbers, the rounded one and what it
             // leaves: with few rows their rounding would not average out, and
@@ -401,11 +403,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float2 v = ml[w * MT * 16 + r];
-            ll += v.y * (v.x == mm ? 1.f : exp2_fast(v.x - mm));
+            ll += v.y * (v.x == mm ? 1.f : exp2_fast((v.x - mm) * sc));
           }
           mt[m][e] = mm;
           lt[m][e] = ll;
-          const float f = mref[m][e] == mm ? 1.f : exp2_fast(mref[m][e] - mm);
+          const float f = mref[m][e] == mm ? 1.f : exp2_fast((mref[m][e] - mm) * sc);
 #pragma unroll
           for (int n = 0; n < DP / 8; ++n) {
             o[m][n][2 * e] *= f;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!done)
                   ln.part_ml[cur.prow + r] = make_float2(mt[m][e], lt[m][e]);
                 else if (a.lse)
-                  a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mt[m][e], lt[m][e]);
+                  a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mt[m][e], lt[m][e], a.scale);
                 if (cur.parts) write_info(a, ln, cur, r, at);
               }
             }

@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the group
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lanes + kOut + t * DP;
-    const float sc = a.scale * 1.44269504088896340736f;
-    const float2 sc2 = make_float2(sc, sc);
+    const float sc = a.scale * kLog2e;
+    const float2 sc2 = make_float2(sc, sc), bias2 = make_float2(ProbBias<T>::value, ProbBias<T>::value);
     // queries of this row tile, 16 bytes a thread, consecutive threads along a
     // row: asynchronous copies, complete after cp_async_wait_all; zeros beyond
     // the group's rows and the head's elements
@@ -534,9 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The weights are taken against the reference maximum as it stands;
             // a tile's own maximum is not looked for. Only when a row's weights
             // add up to more than kSumMost (none can pass it then, so none
-            // overflows) is the reference moved to the maximum and the tile,
-            // still in tensor memory, done again. The first tile sets it
-            // beforehand.
+            // overflows), or a row that has no reference yet sees keys, is the
+            // reference moved to the maximum and the tile, still in tensor
+            // memory, done again: once, after which no weight passes 2^bias.
+            // The first tile sets it beforehand.
             auto mask = [&](uint32_t(&v)[32], int c) {
               if (edge) {
 #pragma unroll
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             bool move = i == 0;
 #pragma unroll 1
-            while (true) {
+            while (true) {  // a pass that moves the reference is the last
               if (move) {
                 float m = -INFINITY;
 #pragma unroll 1
@@ -560,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int e = 0; e < 32; ++e) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(v[e]));
                   m = fmaxf(mx[0], mx[1]);
                 }
-                const float mn = fmaxf(mref, m * sc);
-                const float f = mref == mn ? 1.f : exp2_fast(mref - mn);
+                const float mn = fmaxf(mref, m);
+                const float f = mref == mn ? 1.f : exp2_fast((mref - mn) * sc);
                 mref = mn;
                 l2.x *= f;
                 l2.y *= f;
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_st_wait();
                 }
               }
-              const float ref = (mref == -INFINITY ? 0.f : mref) - ProbBias<T>::value;
+              const float ref = mref == -INFINITY ? 0.f : mref;
               const float2 nref = make_float2(-ref, -ref);
               lt = lrt = make_float2(0.f, 0.f);
               uint32_t sr[2][32];
@@ -599,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mask(v, c);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  float2 w = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, nref);
+                  float2 w = fadd2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), nref);
+                  w = ffma2(w, sc2, bias2);
                   w.x = exp2_fast(w.x);
                   w.y = exp2_fast(w.y);
                   lt = fadd2(lt, w);
@@ -608,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (c < 3) tmem_ld_wait_for(sr[(c + 1) & 1]);
               }
-              move = __any_sync(0xffffffffu, lt.x + lt.y > kSumMost);
+              if (move) break;
+              move = __any_sync(0xffffffffu, lt.x + lt.y > kSumMost || (mref == -INFINITY && k0 < seen));
               if (!move) break;
             }
             l2 = fadd2(l2, lt);
@@ -700,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!done)
               ln.part_ml[cur->prow + r] = make_float2(mref, l);
             else if (a.lse)
-              a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l);
+              a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l, a.scale);
             if (cur->parts) write_info(a, ln, *cur, r, at);
           }
         }
