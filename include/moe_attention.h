@@ -160,7 +160,8 @@ typedef struct {
 moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride, const moe_attn_batch_t* batch,
                               void* out, int64_t out_stride, float* lse, void* stream);
 
-/* Synchronises `stream` and reports (then clears) what the kernels recorded:
+/* Synchronises `stream` and reports (then clears) the first of what the
+ * handle's kernels recorded, on this stream or on others, since the last report:
  * MOE_ERR_INVALID_ARG for a slot, page, length or offset out of range,
  * MOE_ERR_TIMEOUT if a bounded wait gave up, MOE_ERR_CUDA on a CUDA error. */
 moe_status_t moe_attn_sync(moe_attn_t* attn, void* stream);

@@ -1,0 +1,50 @@
+"""The attention operators on streams beside one another."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+from test_gpu_attention import F16, _cuda  # noqa: E402,F401
+from w4a16_routed_expert_gb300 import capi  # noqa: E402
+from w4a16_routed_expert_gb300.attention import PagedAttention  # noqa: E402
+
+
+def test_a_report_on_one_stream_leaves_a_forward_on_another_alone():
+    """Appends with a bad slot are reported again and again while forwards of
+    the same handle run: some words of each stand between its kernels and its
+    join at any time, and none of them may go."""
+    Hk, D, page, seqs, n = 8, 64, 16, 64, 3000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    pages = -(-n // page)
+    kc, vc = (torch.randn(seqs * pages, page, Hk, D, generator=gen, device="cuda").half() for _ in range(2))
+    a = PagedAttention(num_q_heads=Hk, num_kv_heads=Hk, head_dim=D, max_tokens=seqs, max_seqs=seqs, k_cache=kc, v_cache=vc)
+    q = torch.randn(seqs, Hk, D, generator=gen, device="cuda").half()
+    args = dict(q_offsets=torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), max_q_len=1, max_seq_len=n,
+                seq_lens=torch.full((seqs,), n, dtype=torch.int32, device="cuda"),
+                block_table=torch.arange(seqs * pages, dtype=torch.int32, device="cuda").view(seqs, pages))
+    want = a.forward(q, **args)
+    a.sync()
+    outs = torch.empty(400, seqs, Hk, D, dtype=F16, device="cuda")
+    x = torch.ones(1, Hk, D, dtype=F16, device="cuda")
+    zero, beyond = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in (0, kc.shape[0] * page))
+    torch.cuda.synchronize()
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    end = torch.cuda.Event()
+    with torch.cuda.stream(s):
+        for o in outs:
+            a.forward(q, out=o, **args)
+        end.record()
+    reports = 0
+    with torch.cuda.stream(other):
+        while not end.query():
+            a.append(None, x, x, zero, beyond)
+            with pytest.raises(capi.MoEError) as e:
+                a.sync(other)
+            assert e.value.status == capi.MOE_ERR_INVALID_ARG
+            reports += 1
+    torch.cuda.synchronize()
+    assert reports > 3
+    assert all(torch.equal(o, want) for o in outs)
+    a.sync()
+    assert float(want.abs().max()) > 0

@@ -244,18 +244,25 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
                 few_own) && fits;
   }
   if (!fits) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens and lengths beyond what one call takes", fn);
+  // The join sets the words that it reads back to zero. Without it what the
+  // kernels before it left is cleared behind them, on their own stream.
+  auto failed = [&](cudaError_t e) {
+    const size_t words = (size_t)h->cfg.max_tokens * h->cfg.num_q_heads * sizeof(int2);
+    for (int2* info : h->info) cudaMemsetAsync(info, 0, words, s);
+    return cuda_error(e, fn);
+  };
   if (tile.n_cta) {
     const cudaError_t e = moe::launch_attn_tile(h->tile_k, h->tile_v, a, tile, h->box_tile, bf16, s, h->pdl);
-    if (e != cudaSuccess) return cuda_error(e, fn);
+    if (e != cudaSuccess) return failed(e);
   }
   if (few.n_cta) {
     // behind the tile kernel it need not wait for its results, only not end before it
     const cudaError_t e = moe::launch_attn_rows(h->rows_k, h->rows_v, a, few, plan, h->box_rows, bf16,
                                                 tile.n_cta && h->pdl, s, h->pdl);
-    if (e != cudaSuccess) return cuda_error(e, fn);
+    if (e != cudaSuccess) return failed(e);
   }
   const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
-  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+  return e == cudaSuccess ? MOE_OK : failed(e);
 }
 
 }  // namespace
@@ -513,15 +520,16 @@ moe_status_t moe_attn_sync(moe_attn_t* h, void* stream) {
   const char* fn = "moe_attn_sync";
   const moe_status_t st = check_handle(h, fn);
   if (st != MOE_OK) return st;
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  // Only this stream is waited for and nothing but the error word is touched:
+  // a forward may be under way on another.
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaStreamSynchronize(s);
   uint32_t err = 0;
-  if (e == cudaSuccess) e = cudaMemcpy(&err, h->err, 4, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&err, h->err, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess && err) {
-    e = cudaMemset(h->err, 0, 4);
-    // a forward that gave up may have left words that its join did not read
-    const size_t words = (size_t)h->cfg.max_tokens * h->cfg.num_q_heads * sizeof(int2);
-    for (int i = 0; i < 2 && h->info[i] && e == cudaSuccess; ++i) e = cudaMemset(h->info[i], 0, words);
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    e = cudaMemsetAsync(h->err, 0, 4, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   }
   if (e != cudaSuccess) return cuda_error(e, fn);
   if (err == moe::kAttnErrTimeout) return set_error(MOE_ERR_TIMEOUT, "%s: a device-side wait gave up", fn);
