@@ -181,7 +181,7 @@ class PagedAttention:
             op, os_ = self._rows("out", out, T, self.num_q_heads)
         if lse is None and return_lse:
             lse = torch.empty((T, self.num_q_heads), dtype=torch.float32, device=q.device)
-        if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
+        if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous()
                                 or lse.shape != (T, self.num_q_heads)):
             raise ValueError(f"lse: contiguous cuda float32 [{T}][{self.num_q_heads}]")
         bt, ts = None, 0
