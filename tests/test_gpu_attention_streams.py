@@ -48,3 +48,33 @@ def test_a_report_on_one_stream_leaves_a_forward_on_another_alone():
     assert all(torch.equal(o, want) for o in outs)
     a.sync()
     assert float(want.abs().max()) > 0
+
+
+def test_outputs_of_a_call_on_a_given_stream_have_memory_of_that_stream():
+    """Memory that the current stream has freed, but will still write, is not
+    handed to a call on another stream."""
+    H, D, page = 4, 64, 16
+    kc, vc = (torch.zeros(4, page, H, D, device="cuda").half() for _ in range(2))
+    a = PagedAttention(num_q_heads=H, num_kv_heads=H, head_dim=D, rotary_dim=D, max_tokens=8, max_seqs=8, k_cache=kc, v_cache=vc)
+    x = torch.randn(8, H, D, device="cuda").half()
+    pos = torch.arange(8, dtype=torch.int32, device="cuda")
+    batch = dict(q_offsets=torch.arange(9, dtype=torch.int32, device="cuda"), max_q_len=1, seq_lens=pos, max_seq_len=8,
+                 block_table=torch.zeros(8, 1, dtype=torch.int32, device="cuda"))
+    s = torch.cuda.Stream()
+
+    def calls(stream):
+        q, k = a.rotate(x, x, pos, stream=stream)
+        return (q, k, a.append(x, x, x, pos, pos, stream=stream)) + a.forward(x, return_lse=True, stream=stream, **batch)
+
+    want = [t.clone() for t in calls(None)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        freed = [torch.empty_like(t) for t in want]
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for t in freed:
+            t.fill_(9)
+        del freed, t
+        got = calls(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    a.sync()

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import capi
-from .layer import _ptr, _stream_handle
+from .layer import _output, _ptr, _stream_handle
 
 try:  # the handle of a device's current stream without building a Stream object (3 us a call)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
@@ -38,6 +38,10 @@ class PagedAttention:
     "yarn"), "factor" and for yarn "original_max_position" and optionally
     "beta_fast", "beta_slow". scale: of the logits (None: head_dim ** -0.5).
     The tensors must stay alive and in place while the object is used.
+
+    Calls run on the current stream, or on `stream`, which then has to wait for
+    what wrote their inputs (and these must live until it has read them);
+    outputs that a call allocates belong to the stream it runs on.
     """
 
     def __init__(self, *, num_q_heads, num_kv_heads, head_dim, dtype=torch.float16, max_tokens=1, max_seqs=1,
@@ -99,9 +103,9 @@ class PagedAttention:
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         return t.data_ptr(), st if T > 1 else heads * self.head_dim
 
-    def _new_rows(self, like, T, heads):
+    def _new_rows(self, like, T, heads, stream):
         """A new [T][heads][head_dim] tensor, its pointer and token stride."""
-        t = torch.empty((T, heads, self.head_dim), dtype=self.dtype, device=like.device)
+        t = _output((T, heads, self.head_dim), self.dtype, like.device, stream)
         return t, t.data_ptr(), heads * self.head_dim
 
     @staticmethod
@@ -125,13 +129,13 @@ class PagedAttention:
         if q is not None:
             qp, qs = self._rows("q", q, T, self.num_q_heads)
             if q_out is None:
-                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads)
+                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads, stream)
             else:
                 qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
         if k is not None:
             kp, ks = self._rows("k", k, T, self.num_kv_heads)
             if k_out is None:
-                k_out, ko, kos = self._new_rows(k, T, self.num_kv_heads)
+                k_out, ko, kos = self._new_rows(k, T, self.num_kv_heads, stream)
             else:
                 ko, kos = self._rows("k_out", k_out, T, self.num_kv_heads)
         st = self._lib.moe_attn_rotate(self.handle, qp, qs, kp, ks, self._ints("positions", positions, T), T, qo, qos,
@@ -151,7 +155,7 @@ class PagedAttention:
         if q is not None:
             qp, qs = self._rows("q", q, T, self.num_q_heads)
             if q_out is None:
-                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads)
+                q_out, qo, qos = self._new_rows(q, T, self.num_q_heads, stream)
             else:
                 qo, qos = self._rows("q_out", q_out, T, self.num_q_heads)
         kp, ks = self._rows("k", k, T, self.num_kv_heads)
@@ -176,11 +180,11 @@ class PagedAttention:
         T, B = q.shape[0], seq_lens.shape[0]
         qp, qs = self._rows("q", q, T, self.num_q_heads)
         if out is None:
-            out, op, os_ = self._new_rows(q, T, self.num_q_heads)
+            out, op, os_ = self._new_rows(q, T, self.num_q_heads, stream)
         else:
             op, os_ = self._rows("out", out, T, self.num_q_heads)
         if lse is None and return_lse:
-            lse = torch.empty((T, self.num_q_heads), dtype=torch.float32, device=q.device)
+            lse = _output((T, self.num_q_heads), torch.float32, q.device, stream)
         if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous()
                                 or lse.shape != (T, self.num_q_heads)):
             raise ValueError(f"lse: contiguous cuda float32 [{T}][{self.num_q_heads}]")

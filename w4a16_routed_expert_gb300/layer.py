@@ -22,6 +22,19 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
     return s.cuda_stream
 
 
+def _output(shape, dtype, device, stream: Optional[torch.cuda.Stream]):
+    """A new tensor that a call on `stream` (None: the current one) writes. It
+    is allocated on that stream, whose earlier work alone may still use the
+    memory, and its memory also waits for the current stream's work when it is
+    freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 class MoELayer:
     """One routed-expert layer bound to device-resident weights.
 
