@@ -24,6 +24,9 @@ class Tensor:
     def get_device(self):
         return 0
 
+    def __getitem__(self, at):
+        return self._on_cpu[at]
+
     def __getattr__(self, name):
         return getattr(self._on_cpu, name)
 

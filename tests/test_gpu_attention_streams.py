@@ -28,8 +28,11 @@ def test_a_report_on_one_stream_leaves_a_forward_on_another_alone():
     outs = torch.empty(400, seqs, Hk, D, dtype=F16, device="cuda")
     x = torch.ones(1, Hk, D, dtype=F16, device="cuda")
     zero, beyond = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in (0, kc.shape[0] * page))
-    torch.cuda.synchronize()
     s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    a.append(None, x, x, zero, beyond)  # its kernel is loaded at its first launch
+    with pytest.raises(capi.MoEError):
+        a.sync()
+    torch.cuda.synchronize()
     end = torch.cuda.Event()
     with torch.cuda.stream(s):
         for o in outs:
@@ -78,3 +81,25 @@ def test_outputs_of_a_call_on_a_given_stream_have_memory_of_that_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(g, w) for g, w in zip(got, want))
     a.sync()
+
+
+def test_outputs_of_a_layer_call_on_a_given_stream_have_memory_of_that_stream():
+    """The same of the routed-expert layer beside these operators."""
+    import gpu_harness as GH
+    from w4a16_routed_expert_gb300 import synth
+
+    ml = GH.upload(synth.make_layer(synth.TINY, seed=3), max_tokens=16)
+    x = torch.from_numpy(synth.make_tokens(synth.TINY.hidden, 16, seed=4)).cuda()
+    want = ml.forward(x).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        freed = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        freed.fill_(9)
+        del freed
+        got = ml.forward(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    ml.sync()
+    ml.close()

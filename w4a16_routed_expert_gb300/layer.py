@@ -75,7 +75,7 @@ class MoELayer:
                 w: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T = x.shape[0]
         if out is None:
-            out = torch.empty_like(x)
+            out = _output(x.shape, x.dtype, x.device, stream)
         capi.check(capi.moe_layer_forward(self.handle, _ptr(x), T, _ptr(out), _ptr(ids), _ptr(w),
                                           _stream_handle(stream)), "moe_layer_forward")
         return out
@@ -95,10 +95,8 @@ class MoELayer:
     def routing(self, T: int, stream=None):
         dev = torch.device("cuda")
         E, k = self.num_experts, self.top_k
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        perm = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-        inv = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
+        counts, offsets, perm, inv = (_output((n,), torch.int32, dev, stream)
+                                      for n in (E, E + 1, max(T * k, 1), max(T * k, 1)))
         capi.check(capi.moe_layer_routing(self.handle, _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv),
                                           _stream_handle(stream)), "moe_layer_routing")
         return counts, offsets, perm[:T * k], inv[:T * k]
@@ -149,7 +147,7 @@ class MoEStack:
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, states: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
         if out is None:
-            out = torch.empty_like(x)
+            out = _output(x.shape, x.dtype, x.device, stream)
         capi.check(capi.lib().moe_stack_forward(self.handle, _ptr(x), x.shape[0], _ptr(out), _ptr(states),
                                                 _stream_handle(stream)), "moe_stack_forward")
         return out
