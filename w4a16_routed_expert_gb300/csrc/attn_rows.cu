@@ -50,7 +50,22 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int rows, int stag
   return p;
 }
 
+// The computing warps. These barriers have no limit of their own: every
+// computing warp comes to each of them, whatever its bounded waits returned.
 __device__ __forceinline__ void bar_compute() { asm volatile("bar.sync 1, %0;" ::"r"(kWarps * 32) : "memory"); }
+// The same, and whether v holds for any of them.
+__device__ __forceinline__ bool bar_any(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)v), "r"(kWarps * 32)
+      : "memory");
+  return any != 0;
+}
 
 template <typename T, int DP, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -188,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t ph = 0, sph = 0;
     bool ok = true;
     auto next_segment = [&](Segment* s) {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], sph, abort_flag, a.err));
-      if (!got) return false;
+      ok = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], sph, abort_flag, a.err));
+      if (!ok) return false;
       *s = segs[slot_i];
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[slot_i]);
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // queries: rows of 128-byte halves, swizzled as the boxes are; zeros
     // beyond the group's rows and the head's elements
     constexpr int kQ = MT * 16 * DP / 8 / (kWarps * 32);  // 16-byte words of a thread
-    uint4 qv[kQ];
+    uint4 qv[kQ] = {};
     auto load_q = [&](const Segment& s) {
 #pragma unroll
       for (int i = 0; i < kQ; ++i) {
@@ -218,14 +233,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     Segment s;
     bool some = next_segment(&s);
     if (some) load_q(s);
-    while (some) {
+    // A warp whose wait gave up (ok is false; the timeout is recorded, the
+    // results are not looked at) goes through its part's barriers with the
+    // others, and all of them end at the next part's first one. (After the
+    // last part the words stored before it are nobody's.)
+    while (true) {
 #pragma unroll
       for (int i = 0; i < kQ; ++i) {
         const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
         *reinterpret_cast<uint4*>(smem + sp.q + (uint32_t)(c8 >> 3) * MT * 16 * 128 + (uint32_t)r * 128 +
                                   (uint32_t)(((c8 & 7) ^ (r & 7)) << 4)) = qv[i];
       }
-      bar_compute();
+      if (bar_any(!ok) || !some) break;
       float o[MT][DP / 8][4];
       float mref[MT][2], l[MT][2];
       int lim[MT][2];  // keys each of the lane's rows sees
@@ -372,10 +391,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           ph ^= 1u;
         }
       }
-      if (!ok) break;
       // the next part's queries are on their way while this one is joined
       const Segment cur = s;
-      some = next_segment(&s);
+      some = ok && next_segment(&s);
       if (some) load_q(s);
 
       // ---- the four warps' results become one: a common maximum, then the
