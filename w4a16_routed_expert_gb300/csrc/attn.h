@@ -73,6 +73,7 @@ struct LineArgs {
   int weight;
   int has_prefix, has_own;
   int joined;            // the prefix's tiles stand at the front of every own group (has_prefix is 0)
+  int own_most;          // most places that one key head's own groups can have (line_own_places)
   int n_cta;
   int part_rows;         // rows a partial takes at most: min(row_block, most rows of a group)
   int part_row0;         // this kernel's first row of partials
@@ -85,14 +86,18 @@ struct LineArgs {
 inline long long line_part_rows(const LineArgs& ln, long long T, long long Hq) {
   return (ln.has_prefix + ln.has_own) * T * Hq + (long long)ln.n_cta * ln.part_rows;
 }
-// Most places the line can have.
+// Most places that one key head's own groups can have on the line; most places
+// of the line.
+inline long long line_own_places(const AttnArgs& a, const LineArgs& ln) {
+  const long long rows = (long long)a.T * a.g, kt = ln.key_tile, rb = ln.row_block;
+  return ln.has_own ? (rows / rb + a.B) * ((a.max_seq_len + kt - 1) / kt + ln.weight +
+                                           (ln.joined ? (a.prefix_len + kt - 1) / kt : 0))
+                    : 0;
+}
 inline long long line_places(const AttnArgs& a, const LineArgs& ln) {
   const long long rows = (long long)a.T * a.g, kt = ln.key_tile, rb = ln.row_block;
   const long long prefix = ln.has_prefix ? (rows + rb - 1) / rb * ((a.prefix_len + kt - 1) / kt + ln.weight) : 0;
-  const long long own = ln.has_own ? (rows / rb + a.B) * ((a.max_seq_len + kt - 1) / kt + ln.weight +
-                                                                (ln.joined ? (a.prefix_len + kt - 1) / kt : 0))
-                                 : 0;
-  return (prefix + own) * a.Hk;
+  return (prefix + line_own_places(a, ln)) * a.Hk;
 }
 
 // Tensor maps of one cache tensor: boxes of `slots` slots x 64 elements, or of

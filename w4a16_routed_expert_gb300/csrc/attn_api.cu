@@ -229,7 +229,8 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
     used += moe::line_part_rows(*ln, a.T, a.Hq);
     if (ln->has_prefix) j.prefix_step = ln->part_rows;
     if (own) j.own_step = ln->part_rows;
-    return moe::line_places(a, *ln) <= INT_MAX;
+    ln->own_most = (int)std::min<long long>(moe::line_own_places(a, *ln), INT_MAX - 1);
+    return moe::line_places(a, *ln) < INT_MAX;
   };
   moe::LineArgs tile = {}, few = {};
   moe::AttnRowsPlan plan = {};

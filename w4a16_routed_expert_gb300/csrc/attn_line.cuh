@@ -36,14 +36,18 @@ __device__ __forceinline__ int group_span(const LineArgs& ln, int tiles) { retur
 
 // Whole block (NT threads): own_off[b] = places of one key head's groups
 // before sequence b, in shared memory; returns their total. scratch: NT / 32
-// ints.
+// ints. Sequences that overlap (offsets out of order) can come to more than
+// the host counted on and than 32 bits hold: sums stop one place above
+// own_most, and then there is no work.
 template <int NT, int KT, int RB>
 __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off, int32_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!ln.has_own) return 0;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  int sum = 0;
+  const unsigned most = (unsigned)ln.own_most + 1u;
+  auto add = [&](unsigned x, unsigned y) { return min(x + y, most); };  // (both below 2^31)
+  unsigned sum = 0;
   const int front = front_tiles<KT>(a, ln);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
@@ -53,30 +57,32 @@ __device__ int scan_own(const AttnArgs& a, const LineArgs& ln, int32_t* own_off,
 #pragma unroll 1
     for (int rb = 0; rb < blocks; ++rb) span += group_span(ln, front + tiles_of<KT>(block_keys<RB>(a, q.keys, q.n, rb)));
     own_off[b + 1] = span;
-    sum += span;
+    sum = add(sum, (unsigned)span);
   }
-  int incl = sum;
+  unsigned incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl = add(incl, y);
   }
-  if (lane == 31) scratch[warp] = incl;
+  if (lane == 31) scratch[warp] = (int)incl;
   __syncthreads();
-  int base = incl - sum, total = 0;
+  unsigned base = incl - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) base += scratch[w];
-    total += scratch[w];
+    if (w < warp) base = add(base, (unsigned)scratch[w]);
+    total = add(total, (unsigned)scratch[w]);
   }
   if (tid == 0) own_off[0] = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    base += own_off[b + 1];
-    own_off[b + 1] = base;
+    base = add(base, (unsigned)own_off[b + 1]);
+    own_off[b + 1] = (int)base;
   }
   __syncthreads();
-  return total;
+  if (total < most) return (int)total;
+  if (tid == 0) record_error(a.err, kAttnErrBounds);
+  return 0;
 }
 
 // One block's part of one group, handed through shared memory from the
@@ -198,7 +204,8 @@ struct Walk {
         out->rows = min(RB, s.n * a.g - out->row0);
         out->prow = ln.part_row0 + (int)blockIdx.x * ln.part_rows + out->row0 + s.h * s.n * a.g +
                     (s.b < 0 ? 0 : (ln.has_prefix * a.T + s.t0) * a.Hq);
-        out->parts = lo == first ? (first + nt - 1) / share - (int)blockIdx.x + 1 : 0;
+        // (never more than there are blocks, whatever the lengths do meanwhile)
+        out->parts = lo == first ? min((first + nt - 1) / share, ln.n_cta - 1) - (int)blockIdx.x + 1 : 0;
       }
       // (lengths that change under the kernel move groups, but every step
       // still goes on along the line or to a later group)
