@@ -55,7 +55,7 @@ typedef enum {
   MOE_ROPE_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair slows by factor */
   MOE_ROPE_YARN = 3    /* pairs that turn at least beta_fast times within original_max_position keep f_i, those
                           that turn at most beta_slow times take f_i / factor, a linear ramp over i between;
-                          m = 0.1 ln(factor) + 1 (m = 1 everywhere else) */
+                          m = 0.1 ln(factor) + 1 where factor > 1 (m = 1 everywhere else) */
 } moe_rope_scaling_t;
 
 typedef struct {

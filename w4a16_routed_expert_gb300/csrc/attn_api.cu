@@ -96,7 +96,7 @@ void frequencies(const moe_attn_config_t* c, double* inv, double* m) {
       const double ramp = std::min(std::max((i - lo) / width, 0.0), 1.0);
       inv[i] = inv[i] / f * ramp + inv[i] * (1.0 - ramp);
     }
-    *m = 0.1 * std::log(f) + 1.0;
+    *m = f > 1.0 ? 0.1 * std::log(f) + 1.0 : 1.0;
   }
 }
 
