@@ -75,7 +75,7 @@ typedef struct {
   double rope_beta_fast; /* MOE_ROPE_YARN only (0: 32) */
   double rope_beta_slow; /* MOE_ROPE_YARN only (0: 1) */
   double norm_eps;       /* >= 0 */
-  double scale;          /* of the logits; 0: 1 / sqrt(D) */
+  double scale;          /* of the logits, 1e-44 to 2e38; 0: 1 / sqrt(D) */
   /* cache: element (page, slot, head, d) of k_cache and of v_cache is at
    * page * page_stride + slot * slot_stride + head * head_stride + d
    * (elements; each stride a positive multiple of 8). */

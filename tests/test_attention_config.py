@@ -19,3 +19,12 @@ def test_yarn_grows_cosine_and_sine_only_where_it_stretches(lib, factor, m):  # 
     c = config(rope_scaling=capi.MOE_ROPE_YARN, rope_factor=factor)
     assert lib.moe_attn_frequencies(ctypes.byref(c), None, ctypes.byref(got)) == capi.MOE_OK
     assert got.value == pytest.approx(m, rel=1e-14)
+
+
+@pytest.mark.parametrize("scale", [1e-46, 5e-324, 3e38, 1e300])
+def test_a_scale_beyond_32_bits_is_refused(lib, scale):  # noqa: F811
+    """In the kernels it would be zero or infinity, and every output NaN."""
+    h = ctypes.c_void_p(1)
+    buf = capi.moe_attn_buffers_t(k_cache=4096, v_cache=8192)
+    assert lib.moe_attn_create(ctypes.byref(config(scale=scale)), ctypes.byref(buf), ctypes.byref(h)) == capi.MOE_ERR_INVALID_ARG
+    assert h.value is None and "scale" in capi.last_error()

@@ -115,6 +115,9 @@ moe_status_t validate(const moe_attn_config_t* c, const moe_attn_buffers_t* b) {
     return set_error(MOE_ERR_INVALID_ARG, "norm_eps=%g must not be negative", c->norm_eps);
   if (!std::isfinite(c->scale) || c->scale < 0.0)
     return set_error(MOE_ERR_INVALID_ARG, "scale=%g must not be negative", c->scale);
+  // zero or infinite in FP32, it would make NaN of masked logits or of the largest
+  if (c->scale > 0.0 && (c->scale < 1e-44 || c->scale > 2e38))
+    return set_error(MOE_ERR_INVALID_ARG, "scale=%g must be 0 or from 1e-44 to 2e38", c->scale);
   if ((reinterpret_cast<uintptr_t>(b->q_norm) | reinterpret_cast<uintptr_t>(b->k_norm)) % 16)
     return set_error(MOE_ERR_INVALID_ARG, "q_norm and k_norm must be 16-byte aligned");
   if (c->reserved != 0) return set_error(MOE_ERR_INVALID_ARG, "reserved must be 0");
