@@ -17,7 +17,12 @@
  *            prefix shared by every sequence, then each sequence's own keys
  *              o = sum_j e^(s_j) v_j / sum_j e^(s_j),  s_j = scale * q . k_j
  *              lse = ln sum_j e^(s_j)
- *            each key of the prefix is read once for the whole batch
+ *            A row is a query token and one of the query heads of a key head.
+ *            The prefix's keys of a key head are read once for every block of
+ *            rows of all tokens: 256 of them, or 16 (32 at head sizes to 64)
+ *            where few rows read a key; where the batch has as many tokens as
+ *            fill a block of 256 rows for each sequence on average, once for
+ *            every block of each sequence's rows, together with its own keys
  *
  * Frequencies: f_i = theta^(-2i/rotary_dim), scaled for long contexts by
  * moe_rope_scaling_t. An angle p * f_i is reduced to a fraction of a turn in

@@ -21,7 +21,6 @@ struct Half16<__half> {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 };
 template <>
 struct Half16<__nv_bfloat16> {
@@ -32,7 +31,6 @@ struct Half16<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 };
 
 // A sequence of the batch: its query tokens [t0, t0 + n) and its own keys,
