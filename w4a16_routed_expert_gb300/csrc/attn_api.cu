@@ -202,8 +202,9 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
   // Sequences of a row block and more on average: no block would serve two of
   // them, so the prefix is read in one go with the own keys (one partial
-  // instead of two; four chunks of 770 tokens behind 8200 keys:
-  // 382 us so, 413 apart).
+  // instead of two; four chunks of 770 tokens behind 8200 keys: 370 us so, 417
+  // apart). The average is what the host knows: a batch of one long chunk and
+  // many short ones may pass too, and then reads the prefix for each.
   const bool joined = tile_own && tile_prefix && (long long)a.T * a.g >= (long long)a.B * moe::kTileRows;
   moe::JoinArgs j = {};
   j.a = a;

@@ -14,16 +14,18 @@
 // token and keeps in registers over all the heads it takes.
 //
 // Angles: freq is the turns per position as a 64-bit fraction, so position *
-// freq modulo 2^64 is the angle's fraction of a turn, exact at any position;
-// its top 32 bits as a signed number give an angle in [-pi, pi), where the
+// freq modulo 2^64 is the angle's fraction of a turn, off by the frequency's
+// own rounding alone (2^-56 of a turn a position at most); its top 32 bits as a signed number give an angle in [-pi, pi), where the
 // hardware sine and cosine are within 2^-21.4 absolute, far inside the 16-bit
 // rounding of the result (2^-12 relative).
 //
 // Measured (FP16, 16 query and 16 key heads of 128, norm, 8192 tokens): rotate
 // 28 us = 4.8 TB/s, append with the values 37 us = 5.4 TB/s (0.70 and 0.80 of
-// the measured copy rate); one token 2.7 us. Issue slots and the angles of
-// each warp stand beside the bytes: more heads in flight (U = 4: 32 us) or more
-// warps (48 registers, spills: 34 us) are slower.
+// the measured copy rate); one token 2.7 us. At 8192 tokens half of the issue
+// slots are used; the warps wait for loads and for shuffles. 32 warps of two
+// 512-byte loads are 32 KB in flight an SM, short of what the copy rate takes:
+// but more heads in flight (U = 4: 32 us) or more warps (48 registers, spills:
+// 34 us) are slower.
 #include <algorithm>
 
 #include "attn_dev.cuh"

@@ -9,7 +9,7 @@
 // its 16-row tiles cost ~150 issue slots, spread over the SM's eight computing
 // warps. That leaves room to multiply the probabilities in two 16-bit parts.
 // Measured: 32 sequences of up to 24000 own keys, 8 key heads of 128 (1.53
-// GB), 225 us = 6.8 TB/s, the measured copy rate; 16 behind 4099
+// GB), 228 us = 6.7 TB/s, 0.99 of the measured copy rate; 16 behind 4099
 // shared keys with up to 1000 own (92 MB) 25 us: 4 us until the first copy
 // (two dependent loads, then the page's number), 12 us of copies at full rate,
 // 1.5 us to end each part, 4 us for the join.

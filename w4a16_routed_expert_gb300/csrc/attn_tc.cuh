@@ -158,15 +158,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // rounded by itself, a weight at the maximum is off by that rounding: any
 // power of two where m * sc passes 2^24 (FP16 infinity from 2^28). The
 // difference is exact at the maximum and rounded once elsewhere, so no weight
-// passes 2^bias while m is the maximum. The operation more costs 2 to 3% where
-// the softmax counts (four chunks of 770 tokens 374 -> 382 us, 48 sequences of
-// drafts 47.3 -> 48.3 us); taking m from the logits beforehand, only where it
-// is far from zero, costs as much.
+// passes 2^bias while m is the maximum. The operation more costs 1 to 2% where
+// the softmax counts (four chunks of 770 tokens 374 -> 377 to 382 us, 48
+// sequences of drafts 47.3 -> 48.3 us); taking m from the logits beforehand,
+// only where it is far from zero, costs as much.
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // A probability is stored in the 16-bit type times 2^bias. FP16: 2^7, so that
-// weights down to 2^-31 of the reference stay normal numbers, and with the
-// reference maximum at most 2^8 below the true one (kLazy) nothing passes
+// weights down to 2^-21 of the reference are normal numbers (to 2^-31 not
+// zero), and with the reference maximum at most 2^8 below the true one (kLazy) nothing passes
 // 2^15. BF16 has FP32's range.
 template <typename T>
 struct ProbBias {

@@ -11,8 +11,8 @@
 // measured copy rate): up to ~190 rows the keys' bytes bound it, above that
 // the products.
 // Measured: four chunks of 301 to 1024 tokens behind 8200 keys, 32 query and 8
-// key heads of 128, 345 us = 1.37 PFLOP/s, 0.71 of the measured bf16 rate; a
-// key tile then takes 2700 to 2950 cycles. P V runs at the tensor cores' rate
+// key heads of 128, 370 us = 1.30 PFLOP/s, 0.67 of the measured bf16 rate; a
+// key tile took 2700 to 2950 cycles when that was 361 us. P V runs at the tensor cores' rate
 // (64 cycles an MMA), Q K^T, which reads both operands from shared memory, at
 // ~95; the softmax of a row tile takes 1000 to 1300 and hides.
 //
@@ -754,8 +754,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
 // 64-bit results the outputs of many rows together are 1.35 times as far off
 // as rounding alone would leave them; a few rows by themselves, with a few
 // hundred keys, up to 1.8 times, or 1.4 with the quotient by the rounded sum,
-// which costs up to 8% (four chunks of 770 tokens: 402 us against 366). Below
-// 4096 rows it is taken.
+// which costs about 10% (four chunks of 770 tokens 406 us against 370, 64
+// sequences behind 32768 keys 92 against 83). Below 4096 rows it is taken.
 template <typename T>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int bl,
                      cudaStream_t s, bool pdl) {
