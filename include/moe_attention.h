@@ -2,7 +2,7 @@
  * moe_attention.h — C ABI of the attention operators that stand beside the
  * routed-expert layer in a decoder block (GB300, sm_103a).
  *
- * Three operators over one handle, in the order a decoder block runs them:
+ * Operators over one handle. Three in the order a decoder block runs them:
  *
  *   rotate   RMS norm of every query and key head, then the rotary rotation
  *              y[d]  = x[d] * rsqrt(mean_d x^2 + eps) * w[d]     (w given)
@@ -24,6 +24,16 @@
  *            fill a block of 256 rows for each sequence on average, once for
  *            every block of each sequence's rows, together with its own keys
  *
+ * and, around a step that checks trees of drafted tokens (the lengths then
+ * stand on the GPU, where it is first known how many were right):
+ *
+ *   plan     offsets, positions, cache slots, block table entries and the
+ *            trees' masks, from lengths, parents and a ring of free pages
+ *   forward_tree  forward where a token sees, behind its sequence's context,
+ *            the tokens of its own branch
+ *   accept   the branch that the model's choices confirm
+ *   keep     that branch's keys and values moved behind the context
+ *
  * Frequencies: f_i = theta^(-2i/rotary_dim), scaled for long contexts by
  * moe_rope_scaling_t. An angle p * f_i is reduced to a fraction of a turn in
  * 64-bit fixed point, so it keeps its accuracy at any 32-bit position.
@@ -39,8 +49,8 @@
  * (moe_layer_last_error(NULL) describes the calling thread's last failure),
  * device pointers are borrowed, calls are asynchronous on the given CUDA
  * stream and allocate nothing, so they can be captured in a CUDA graph. One
- * forward at a time per handle (two that overlap share its workspace);
- * rotate and append use none of it. Kernels never trap and every device-side
+ * forward and one plan at a time per handle (two that overlap share its
+ * workspace); the others use none of it. Kernels never trap and every device-side
  * wait is bounded; moe_attn_sync reports what they recorded.
  */
 #ifndef MOE_ATTENTION_H
@@ -164,6 +174,98 @@ typedef struct {
  * undefined, memory outside the cache is not touched. */
 moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride, const moe_attn_batch_t* batch,
                               void* out, int64_t out_stride, float* lse, void* stream);
+
+/* moe_attn_forward where the new tokens of each sequence are the nodes of a
+ * tree (or any set of which each sees some): of its sequence's n keys, the last
+ * m of which are its m query tokens', token i sees the first n - m and key
+ * n - m + j where bit j % 32 of tree[token * tree_stride + j / 32] is set; a
+ * row with no bit sees not even itself. Bits from m on are ignored. The prefix
+ * is seen by all; batch->causal is not looked at.
+ *   tree         device [T][tree_stride]
+ *   tree_stride  words of a token, at least max_q_len / 32 rounded up;
+ *                T * tree_stride below 2^31
+ * NULL with max_seq_len 0 (there are no own keys). */
+moe_status_t moe_attn_forward_tree(moe_attn_t* attn, const void* q, int64_t q_stride, const moe_attn_batch_t* batch,
+                                   const uint32_t* tree, int32_t tree_stride, void* out, int64_t out_stride, float* lse,
+                                   void* stream);
+
+/* The tables of one step. Sequence b holds context_lens[b] own keys in
+ * state[2 + b] pages and adds new_lens[b] tokens; the pages that they need
+ * beyond those are taken from the free ones in order of sequences, and a
+ * sequence that ends gives all of its pages back (free from the next step on).
+ * Where the free pages do not reach for a sequence that needs some, neither it
+ * nor any later one that needs some is served: it gets no pages, no slots and
+ * seq_lens 0, and its tokens see the prefix alone.
+ * All arrays are on the device. */
+typedef struct {
+  int32_t num_seqs;            /* B, 0..4096 */
+  int32_t num_tokens;          /* T, 0..2^22: room of the tokens' outputs, at least the sum of new_lens */
+  int32_t max_nodes;           /* most new tokens of a tree, 0..1024; 0: no trees */
+  int32_t prefix_len;          /* position of the first own key, 0..2^30 */
+  const int32_t* context_lens; /* [B] */
+  const int32_t* new_lens;     /* [B], 0 or more; -1: the sequence ends */
+  const int32_t* parents;      /* [T] with max_nodes: the new token, counted within the sequence and before this
+                                  one, that each continues; -1: the context */
+  int32_t* block_table;        /* [B][table_stride]: new entries are written */
+  int32_t table_stride;        /* at least 1 */
+  int32_t free_capacity;       /* F: places of the ring, at least as many as there are pages in use */
+  int32_t* free_pages;         /* [F]: the free pages are those at (first + i) % F, i < count */
+  const int32_t* state;        /* [2 + B]: first, count, then the pages that each sequence holds */
+  int32_t* state_out;          /* [2 + B]: after the step; may be state */
+  int32_t* q_offsets;          /* out [B + 1]: each sequence's first token */
+  int32_t* seq_lens;           /* out [B]: context_lens + new_lens; 0 for one that ends or is not served */
+  int32_t* positions;          /* out [T]: prefix_len + context + place in the line, or depth in the tree */
+  int32_t* slots;              /* out [T]: of key context + place; -1: not served */
+  uint32_t* tree;              /* out [T][ceil(max_nodes / 32)]: a token's branch (moe_attn_forward_tree); NULL without */
+} moe_attn_plan_t;
+
+/* Fills a step's tables. Tokens behind the last sequence get position 0, slot
+ * -1 and no bits; ring places and table entries that the step does not give out
+ * or take back stay as they were. One plan at a time per handle. A length,
+ * parent, page or count out of range (a context that is negative, a sequence
+ * longer than its row of the table, more tokens than T or max_nodes, a parent
+ * not before its child, a free page beyond the cache) is recorded (moe_attn_sync:
+ * MOE_ERR_INVALID_ARG); such a sequence is not served, such a token has slot -1
+ * or no parent. */
+moe_status_t moe_attn_plan(moe_attn_t* attn, const moe_attn_plan_t* plan, void* stream);
+
+/* The confirmed branch of each sequence's tree. Node 0 is the token that was
+ * decided before; from an accepted node i the branch goes on to the first later
+ * node whose parent is i and whose token is targets[i]. */
+typedef struct {
+  int32_t num_seqs;            /* B, 0..2^20 */
+  int32_t num_tokens;          /* T, 0..2^22 */
+  int32_t max_path;            /* P, 1..2^20: longest branch taken */
+  int32_t reserved;            /* 0 */
+  const int32_t* q_offsets;    /* device [B + 1] */
+  const int32_t* parents;      /* device [T], counted within the sequence */
+  const int32_t* tokens;       /* device [T]: what was drafted */
+  const int32_t* targets;      /* device [T]: the model's choice after each token */
+  const int32_t* seq_lens;     /* device [B] or NULL: a sequence with fewer keys than tokens (it was not served)
+                                  accepts nothing */
+  const int32_t* context_lens; /* device [B] */
+  int32_t* path;               /* out [B][P]: the branch's nodes, then -1 */
+  int32_t* counts;             /* out [B]: nodes of the branch */
+  int32_t* next_tokens;        /* out [B]: targets of its last node; -1 where there is none */
+  int32_t* context_out;        /* out [B]: context_lens + counts; may be context_lens */
+} moe_attn_accept_t;
+
+/* Uses no cache: a handle without one will do. An offset out of order or
+ * beyond T is recorded (MOE_ERR_INVALID_ARG) and clamped. */
+moe_status_t moe_attn_accept(moe_attn_t* attn, const moe_attn_accept_t* accept, void* stream);
+
+/* Moves the keys and values of each sequence's accepted nodes: those of node
+ * path[b][i] to key seq_lens[b] - m + i for i < counts[b], m the sequence's
+ * tokens; in the caches of all n handles, which must be of one shape, type and
+ * strides and no cache twice.
+ *   path    device [num_seqs][path_stride], ascending from i or more
+ *   counts  device [num_seqs]
+ * Errors are recorded in attns[0]: a path or count out of order or range, a
+ * page beyond the cache; what stands before it in the path is moved. */
+moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs, const int32_t* q_offsets,
+                           const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
+                           int32_t table_stride, const int32_t* path, int32_t path_stride, const int32_t* counts,
+                           void* stream);
 
 /* Synchronises `stream` and reports (then clears) the first of what the
  * handle's kernels recorded, on this stream or on others, since the last report:

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_w4a16.so")
 SOURCES = ["route.cu", "route_static.cu", "gemv.cu", "decode.cu", "decode1.cu", "gemm.cu", "moe_layer.cu", "stack.cu", "residency.cu", "slot_planner.cpp", "expert_cache.cpp",
-           "attn_api.cu", "attn_rope.cu", "attn_rows.cu", "attn_tile.cu", "attn_join.cu"]
+           "attn_api.cu", "attn_rope.cu", "attn_rows.cu", "attn_tile.cu", "attn_join.cu",
+           "attn_plan.cu", "attn_accept.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + [

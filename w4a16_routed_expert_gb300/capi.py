@@ -79,6 +79,19 @@ class moe_attn_batch_t(ctypes.Structure):
                 ("prefix_pages", ctypes.c_void_p), ("causal", ctypes.c_int32)]
 
 
+class moe_attn_plan_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "num_tokens", "max_nodes", "prefix_len")] + [
+        (n, ctypes.c_void_p) for n in ("context_lens", "new_lens", "parents", "block_table")] + [
+        ("table_stride", ctypes.c_int32), ("free_capacity", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "free_pages", "state", "state_out", "q_offsets", "seq_lens", "positions", "slots", "tree")]
+
+
+class moe_attn_accept_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "num_tokens", "max_path", "reserved")] + [
+        (n, ctypes.c_void_p) for n in ("q_offsets", "parents", "tokens", "targets", "seq_lens", "context_lens", "path",
+                                       "counts", "next_tokens", "context_out")]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status
@@ -125,6 +138,10 @@ PROTOTYPES = {
     "moe_attn_rotate": (_I32, [_P, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _P, _I64, _P]),
     "moe_attn_append": (_I32, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P]),
     "moe_attn_forward": (_I32, [_P, _P, _I64, ctypes.POINTER(moe_attn_batch_t), _P, _I64, _P, _P]),
+    "moe_attn_forward_tree": (_I32, [_P, _P, _I64, ctypes.POINTER(moe_attn_batch_t), _P, _I32, _P, _I64, _P, _P]),
+    "moe_attn_plan": (_I32, [_P, ctypes.POINTER(moe_attn_plan_t), _P]),
+    "moe_attn_accept": (_I32, [_P, ctypes.POINTER(moe_attn_accept_t), _P]),
+    "moe_attn_keep": (_I32, [ctypes.POINTER(_P), _I32, _I32, _P, _P, _I32, _P, _I32, _P, _I32, _P, _P]),
     "moe_attn_sync": (_I32, [_P, _P]),
     "moe_attn_destroy": (_I32, [_P]),
     # include/moe_residency.h

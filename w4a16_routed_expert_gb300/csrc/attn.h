@@ -49,6 +49,8 @@ struct AttnArgs {
   int T, B, Hq, Hk, g, D;
   const int32_t *q_offsets, *seq_lens, *block_table, *prefix_pages;
   int table_stride, prefix_len, causal, max_q_len, max_seq_len;
+  const uint32_t* tree;  // nullable: [T][tree_words], bit j of a token's row: it sees its sequence's token j (causal is 0)
+  int tree_words;
   float scale;           // of the logits
   void* out;
   long long out_stride;
@@ -151,5 +153,41 @@ struct JoinArgs {
   int DP;
 };
 cudaError_t launch_attn_join(const JoinArgs& j, bool bf16, cudaStream_t s, bool pdl);
+
+// A step's tables (moe_attn_plan_t).
+struct PlanArgs {
+  int B, T, max_nodes, words, prefix_len;
+  const int32_t *context_lens, *new_lens, *parents;
+  int32_t* block_table;
+  int table_stride, ring_size, page_size, num_pages;
+  int32_t* free_pages;
+  const int32_t* state;
+  int32_t* state_out;
+  int32_t *q_offsets, *seq_lens, *positions, *slots;
+  uint32_t* tree;
+  uint32_t* ticket;  // blocks that are done, 0 between plans
+  uint32_t* err;
+};
+cudaError_t launch_attn_plan(const PlanArgs& a, int num_sms, cudaStream_t s, bool pdl);
+
+// The confirmed branch of each tree (moe_attn_accept_t).
+struct AcceptArgs {
+  int B, T, P;
+  const int32_t *q_offsets, *parents, *tokens, *targets, *seq_lens, *context_lens;
+  int32_t *path, *counts, *next_tokens, *context_out;
+  uint32_t* err;
+};
+cudaError_t launch_attn_accept(const AcceptArgs& a, cudaStream_t s, bool pdl);
+
+// Accepted nodes' keys and values of up to kKeepLayers caches to their places.
+constexpr int kKeepLayers = 32;
+struct KeepArgs {
+  void* kv[2 * kKeepLayers];  // keys, values of each layer
+  int layers, B, Hk, D, page_size, num_pages, max_seq_len, table_stride, path_stride;
+  long long page_stride, slot_stride, head_stride;
+  const int32_t *q_offsets, *seq_lens, *block_table, *path, *counts;
+  uint32_t* err;
+};
+cudaError_t launch_attn_keep(const KeepArgs& a, int num_sms, cudaStream_t s, bool pdl);
 
 }  // namespace moe

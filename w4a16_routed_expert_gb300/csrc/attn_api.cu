@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <functional>
 #include <new>
 
 #include "attn.h"
@@ -24,6 +25,7 @@ struct moe_attn {
   float rope_m = 1.f;
   void* ws = nullptr;
   uint32_t* err = nullptr;
+  uint32_t* ticket = nullptr;    // of plan: its blocks that are done
   uint64_t* freq = nullptr;
   // forward's workspace
   int2* info[2] = {};            // [max_tokens][Hq] of the prefix, of own keys: where a row's partials are
@@ -185,8 +187,7 @@ void fill_rope(const moe_attn* h, moe::RopeArgs* a) {
 }
 
 // Enqueue a forward whose arguments have been checked.
-moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
-  const char* fn = "moe_attn_forward";
+moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaStream_t s) {
   const bool bf16 = h->cfg.dtype == MOE_DTYPE_BF16;
   const int own_rows = a.max_seq_len > 0 ? a.max_q_len * a.g : 0;
   const int prefix_rows = a.prefix_len > 0 ? (int)std::min<long long>((long long)a.T * a.g, INT_MAX / 2) : 0;
@@ -270,6 +271,87 @@ moe_status_t forward(moe_attn* h, const moe::AttnArgs& a, cudaStream_t s) {
   return e == cudaSuccess ? MOE_OK : failed(e);
 }
 
+// A forward of the caller's arguments; tree_stride > 0: over trees.
+moe_status_t forward_call(moe_attn* h, const char* fn, const void* q, int64_t q_stride, const moe_attn_batch_t* b,
+                          const uint32_t* tree, int tree_stride, void* out, int64_t out_stride, float* lse,
+                          void* stream) {
+  const bool over_tree = tree_stride > 0;
+  moe_status_t st = check_handle(h, fn);
+  if (st != MOE_OK) return st;
+  const moe_attn_config_t& c = h->cfg;
+  if (!h->buf.k_cache) return set_error(MOE_ERR_INVALID_ARG, "%s: the handle has no cache", fn);
+  if (!b) return set_error(MOE_ERR_INVALID_ARG, "%s: batch must not be NULL", fn);
+  if (b->num_tokens < 0 || b->num_tokens > c.max_tokens)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_tokens=%d out of 0..max_tokens=%d", fn, b->num_tokens,
+                     c.max_tokens);
+  if (b->num_seqs < 0 || b->num_seqs > c.max_seqs)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..max_seqs=%d", fn, b->num_seqs, c.max_seqs);
+  if (b->num_tokens == 0) return MOE_OK;
+  if (b->num_seqs == 0) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
+  if (!q || !out || !b->q_offsets || !b->seq_lens)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: q, out, q_offsets and seq_lens must not be NULL", fn);
+  if (b->max_q_len < 1 || b->max_q_len > b->num_tokens)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_q_len=%d out of 1..num_tokens", fn, b->max_q_len);
+  if ((long long)b->max_q_len * b->num_seqs < b->num_tokens)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_q_len * num_seqs is less than num_tokens", fn);
+  if (b->max_seq_len < 0 || b->prefix_len < 0 || b->table_stride < 0)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len, prefix_len and table_stride must not be negative", fn);
+  if ((long long)b->max_seq_len > (long long)b->table_stride * c.page_size)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len=%d beyond table_stride * page_size", fn, b->max_seq_len);
+  if ((long long)b->max_seq_len + b->prefix_len > (1LL << 30))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: more than 2^30 keys", fn);
+  if (b->max_seq_len > 0 && !b->block_table)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: block_table must not be NULL", fn);
+  if (b->prefix_len > 0 && !b->prefix_pages)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: prefix_pages must not be NULL", fn);
+  if (!over_tree && b->causal != 0 && b->causal != 1) return set_error(MOE_ERR_INVALID_ARG, "%s: causal must be 0 or 1", fn);
+  if (over_tree && b->max_seq_len > 0) {
+    if (!tree || reinterpret_cast<uintptr_t>(tree) % 4)
+      return set_error(MOE_ERR_INVALID_ARG, "%s: tree must be 4-byte aligned and not NULL", fn);
+    if (tree_stride < (b->max_q_len + 31) / 32 || (long long)tree_stride * b->num_tokens > INT_MAX)
+      return set_error(MOE_ERR_INVALID_ARG, "%s: tree_stride=%d: at least max_q_len / 32, num_tokens * it below 2^31", fn,
+                       tree_stride);
+  }
+  st = check_rows(h, fn, "q", q, q_stride, c.num_q_heads);
+  if (st == MOE_OK) st = check_rows(h, fn, "out", out, out_stride, c.num_q_heads);
+  if (st != MOE_OK) return st;
+  moe::AttnArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_cache = h->buf.k_cache;
+  a.v_cache = h->buf.v_cache;
+  a.page_stride = c.page_stride;
+  a.slot_stride = c.slot_stride;
+  a.head_stride = c.head_stride;
+  a.page_size = c.page_size;
+  a.num_pages = (int)c.num_pages;
+  a.T = b->num_tokens;
+  a.B = b->num_seqs;
+  a.Hq = c.num_q_heads;
+  a.Hk = c.num_kv_heads;
+  a.g = c.num_q_heads / c.num_kv_heads;
+  a.D = c.head_dim;
+  a.q_offsets = b->q_offsets;
+  a.seq_lens = b->seq_lens;
+  a.block_table = b->block_table;
+  a.prefix_pages = b->prefix_pages;
+  a.table_stride = b->table_stride;
+  a.prefix_len = b->prefix_len;
+  a.causal = over_tree ? 0 : b->causal;
+  if (over_tree && b->max_seq_len > 0) {
+    a.tree = tree;
+    a.tree_words = tree_stride;
+  }
+  a.max_q_len = b->max_q_len;
+  a.max_seq_len = b->max_seq_len;
+  a.scale = h->scale;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.err = h->err;
+  return forward(h, fn, a, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -305,7 +387,7 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   }
   // workspace: error word, frequencies; with a cache the forward's tables and
   // the blocks' partial rows
-  size_t bytes = align256(4) + align256(64 * 8);
+  size_t bytes = align256(8) + align256(64 * 8);
   const size_t NR = (size_t)config->max_tokens * config->num_q_heads;
   if (buffers->k_cache) {
     h->DP = config->head_dim <= 64 ? 64 : 128;
@@ -335,7 +417,8 @@ moe_status_t moe_attn_create(const moe_attn_config_t* config, const moe_attn_buf
   }
   char* p = static_cast<char*>(h->ws);
   h->err = reinterpret_cast<uint32_t*>(p);
-  p += align256(4);
+  h->ticket = h->err + 1;
+  p += align256(8);
   h->freq = reinterpret_cast<uint64_t*>(p);
   p += align256(64 * 8);
   if (buffers->k_cache) {
@@ -455,70 +538,166 @@ moe_status_t moe_attn_append(moe_attn_t* h, const void* q, int64_t q_stride, con
 
 moe_status_t moe_attn_forward(moe_attn_t* h, const void* q, int64_t q_stride, const moe_attn_batch_t* b, void* out,
                               int64_t out_stride, float* lse, void* stream) {
-  const char* fn = "moe_attn_forward";
-  moe_status_t st = check_handle(h, fn);
+  return forward_call(h, "moe_attn_forward", q, q_stride, b, nullptr, 0, out, out_stride, lse, stream);
+}
+
+moe_status_t moe_attn_forward_tree(moe_attn_t* h, const void* q, int64_t q_stride, const moe_attn_batch_t* b,
+                                   const uint32_t* tree, int32_t tree_stride, void* out, int64_t out_stride, float* lse,
+                                   void* stream) {
+  const char* fn = "moe_attn_forward_tree";
+  if (tree_stride < 1) return set_error(MOE_ERR_INVALID_ARG, "%s: tree_stride=%d must be positive", fn, tree_stride);
+  return forward_call(h, fn, q, q_stride, b, tree, tree_stride, out, out_stride, lse, stream);
+}
+
+moe_status_t moe_attn_plan(moe_attn_t* h, const moe_attn_plan_t* p, void* stream) {
+  const char* fn = "moe_attn_plan";
+  const moe_status_t st = check_handle(h, fn);
   if (st != MOE_OK) return st;
-  const moe_attn_config_t& c = h->cfg;
   if (!h->buf.k_cache) return set_error(MOE_ERR_INVALID_ARG, "%s: the handle has no cache", fn);
-  if (!b) return set_error(MOE_ERR_INVALID_ARG, "%s: batch must not be NULL", fn);
-  if (b->num_tokens < 0 || b->num_tokens > c.max_tokens)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: num_tokens=%d out of 0..max_tokens=%d", fn, b->num_tokens,
-                     c.max_tokens);
-  if (b->num_seqs < 0 || b->num_seqs > c.max_seqs)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..max_seqs=%d", fn, b->num_seqs, c.max_seqs);
-  if (b->num_tokens == 0) return MOE_OK;
-  if (b->num_seqs == 0) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
-  if (!q || !out || !b->q_offsets || !b->seq_lens)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: q, out, q_offsets and seq_lens must not be NULL", fn);
-  if (b->max_q_len < 1 || b->max_q_len > b->num_tokens)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: max_q_len=%d out of 1..num_tokens", fn, b->max_q_len);
-  if ((long long)b->max_q_len * b->num_seqs < b->num_tokens)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: max_q_len * num_seqs is less than num_tokens", fn);
-  if (b->max_seq_len < 0 || b->prefix_len < 0 || b->table_stride < 0)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len, prefix_len and table_stride must not be negative", fn);
-  if ((long long)b->max_seq_len > (long long)b->table_stride * c.page_size)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len=%d beyond table_stride * page_size", fn, b->max_seq_len);
-  if ((long long)b->max_seq_len + b->prefix_len > (1LL << 30))
-    return set_error(MOE_ERR_INVALID_ARG, "%s: more than 2^30 keys", fn);
-  if (b->max_seq_len > 0 && !b->block_table)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: block_table must not be NULL", fn);
-  if (b->prefix_len > 0 && !b->prefix_pages)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: prefix_pages must not be NULL", fn);
-  if (b->causal != 0 && b->causal != 1) return set_error(MOE_ERR_INVALID_ARG, "%s: causal must be 0 or 1", fn);
-  st = check_rows(h, fn, "q", q, q_stride, c.num_q_heads);
-  if (st == MOE_OK) st = check_rows(h, fn, "out", out, out_stride, c.num_q_heads);
-  if (st != MOE_OK) return st;
-  moe::AttnArgs a = {};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.k_cache = h->buf.k_cache;
-  a.v_cache = h->buf.v_cache;
-  a.page_stride = c.page_stride;
-  a.slot_stride = c.slot_stride;
-  a.head_stride = c.head_stride;
-  a.page_size = c.page_size;
-  a.num_pages = (int)c.num_pages;
-  a.T = b->num_tokens;
-  a.B = b->num_seqs;
-  a.Hq = c.num_q_heads;
-  a.Hk = c.num_kv_heads;
-  a.g = c.num_q_heads / c.num_kv_heads;
-  a.D = c.head_dim;
-  a.q_offsets = b->q_offsets;
-  a.seq_lens = b->seq_lens;
-  a.block_table = b->block_table;
-  a.prefix_pages = b->prefix_pages;
-  a.table_stride = b->table_stride;
-  a.prefix_len = b->prefix_len;
-  a.causal = b->causal;
-  a.max_q_len = b->max_q_len;
-  a.max_seq_len = b->max_seq_len;
-  a.scale = h->scale;
-  a.out = out;
-  a.out_stride = out_stride;
-  a.lse = lse;
+  if (!p) return set_error(MOE_ERR_INVALID_ARG, "%s: plan must not be NULL", fn);
+  if (p->num_seqs < 0 || p->num_seqs > 4096)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..4096", fn, p->num_seqs);
+  if (p->num_tokens < 0 || p->num_tokens > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_tokens=%d out of 0..2^22", fn, p->num_tokens);
+  if (p->max_nodes < 0 || p->max_nodes > 1024)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_nodes=%d out of 0..1024", fn, p->max_nodes);
+  if (p->prefix_len < 0 || p->prefix_len > (1 << 30))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: prefix_len=%d out of 0..2^30", fn, p->prefix_len);
+  if (p->table_stride < 1 || p->free_capacity < 1 || p->free_capacity > (1 << 30))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: table_stride=%d must be positive, free_capacity=%d in 1..2^30", fn,
+                     p->table_stride, p->free_capacity);
+  if (!p->free_pages || !p->state || !p->state_out || !p->q_offsets)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: free_pages, state, state_out and q_offsets must not be NULL", fn);
+  if (p->num_seqs > 0 && (!p->context_lens || !p->new_lens || !p->block_table || !p->seq_lens))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: context_lens, new_lens, block_table and seq_lens must not be NULL", fn);
+  if (p->num_tokens > 0 && (!p->positions || !p->slots || (p->max_nodes > 0 && (!p->parents || !p->tree))))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: positions, slots and, with trees, parents and tree must not be NULL", fn);
+  moe::PlanArgs a = {};
+  a.B = p->num_seqs;
+  a.T = p->num_tokens;
+  a.max_nodes = p->max_nodes;
+  a.words = (p->max_nodes + 31) / 32;
+  a.prefix_len = p->prefix_len;
+  a.context_lens = p->context_lens;
+  a.new_lens = p->new_lens;
+  a.parents = p->parents;
+  a.block_table = p->block_table;
+  a.table_stride = p->table_stride;
+  a.ring_size = p->free_capacity;
+  a.page_size = h->cfg.page_size;
+  a.num_pages = (int)h->cfg.num_pages;
+  a.free_pages = p->free_pages;
+  a.state = p->state;
+  a.state_out = p->state_out;
+  a.q_offsets = p->q_offsets;
+  a.seq_lens = p->seq_lens;
+  a.positions = p->positions;
+  a.slots = p->slots;
+  a.tree = p->tree;
+  a.ticket = h->ticket;
   a.err = h->err;
-  return forward(h, a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = moe::launch_attn_plan(a, h->num_sms, static_cast<cudaStream_t>(stream), h->pdl);
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
+moe_status_t moe_attn_accept(moe_attn_t* h, const moe_attn_accept_t* p, void* stream) {
+  const char* fn = "moe_attn_accept";
+  const moe_status_t st = check_handle(h, fn);
+  if (st != MOE_OK) return st;
+  if (!p) return set_error(MOE_ERR_INVALID_ARG, "%s: accept must not be NULL", fn);
+  if (p->num_seqs < 0 || p->num_seqs > (1 << 20))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..2^20", fn, p->num_seqs);
+  if (p->num_tokens < 0 || p->num_tokens > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_tokens=%d out of 0..2^22", fn, p->num_tokens);
+  if (p->max_path < 1 || p->max_path > (1 << 20))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_path=%d out of 1..2^20", fn, p->max_path);
+  if (p->reserved != 0) return set_error(MOE_ERR_INVALID_ARG, "%s: reserved must be 0", fn);
+  if (p->num_seqs == 0) return MOE_OK;
+  if (!p->q_offsets || !p->context_lens || !p->path || !p->counts || !p->next_tokens || !p->context_out)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: only seq_lens may be NULL", fn);
+  if (p->num_tokens > 0 && (!p->parents || !p->tokens || !p->targets))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: parents, tokens and targets must not be NULL", fn);
+  moe::AcceptArgs a = {};
+  a.B = p->num_seqs;
+  a.T = p->num_tokens;
+  a.P = p->max_path;
+  a.q_offsets = p->q_offsets;
+  a.parents = p->parents;
+  a.tokens = p->tokens;
+  a.targets = p->targets;
+  a.seq_lens = p->seq_lens;
+  a.context_lens = p->context_lens;
+  a.path = p->path;
+  a.counts = p->counts;
+  a.next_tokens = p->next_tokens;
+  a.context_out = p->context_out;
+  a.err = h->err;
+  const cudaError_t e = moe::launch_attn_accept(a, static_cast<cudaStream_t>(stream), h->pdl);
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
+moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs, const int32_t* q_offsets,
+                           const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
+                           int32_t table_stride, const int32_t* path, int32_t path_stride, const int32_t* counts,
+                           void* stream) {
+  const char* fn = "moe_attn_keep";
+  if (!attns || n < 1 || n > 1024) return set_error(MOE_ERR_INVALID_ARG, "%s: 1 to 1024 handles, got %d", fn, n);
+  const void* caches[2 * 1024];
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_attn* h = attns[i];
+    const moe_status_t st = check_handle(h, fn);
+    if (st != MOE_OK) return st;
+    if (!h->buf.k_cache) return set_error(MOE_ERR_INVALID_ARG, "%s: handle %d has no cache", fn, i);
+    const moe_attn_config_t &c = h->cfg, &f = attns[0]->cfg;
+    if (c.num_kv_heads != f.num_kv_heads || c.head_dim != f.head_dim || c.dtype != f.dtype ||
+        c.page_size != f.page_size || c.num_pages != f.num_pages || c.page_stride != f.page_stride ||
+        c.slot_stride != f.slot_stride || c.head_stride != f.head_stride)
+      return set_error(MOE_ERR_INVALID_ARG, "%s: the cache of handle %d has another shape, type or strides", fn, i);
+    caches[2 * i] = h->buf.k_cache;
+    caches[2 * i + 1] = h->buf.v_cache;
+  }
+  std::sort(caches, caches + 2 * n, std::less<const void*>());
+  if (std::adjacent_find(caches, caches + 2 * n) != caches + 2 * n)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: the same cache twice", fn);
+  const moe_attn* h = attns[0];
+  if (num_seqs < 0 || num_seqs > 4096)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..4096", fn, num_seqs);
+  if (num_seqs == 0) return MOE_OK;
+  if (!q_offsets || !seq_lens || !block_table || !path || !counts)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: arrays must not be NULL", fn);
+  if (table_stride < 1 || path_stride < 1 || max_seq_len < 0)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: table_stride and path_stride must be positive, max_seq_len not negative",
+                     fn);
+  if ((long long)max_seq_len > (long long)table_stride * h->cfg.page_size)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len=%d beyond table_stride * page_size", fn, max_seq_len);
+  moe::KeepArgs a = {};
+  a.B = num_seqs;
+  a.Hk = h->cfg.num_kv_heads;
+  a.D = h->cfg.head_dim;
+  a.page_size = h->cfg.page_size;
+  a.num_pages = (int)h->cfg.num_pages;
+  a.max_seq_len = max_seq_len;
+  a.table_stride = table_stride;
+  a.path_stride = path_stride;
+  a.page_stride = h->cfg.page_stride;
+  a.slot_stride = h->cfg.slot_stride;
+  a.head_stride = h->cfg.head_stride;
+  a.q_offsets = q_offsets;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.path = path;
+  a.counts = counts;
+  a.err = h->err;
+  for (int32_t i = 0; i < n; i += moe::kKeepLayers) {
+    a.layers = std::min(n - i, moe::kKeepLayers);
+    for (int k = 0; k < a.layers; ++k) {
+      a.kv[2 * k] = attns[i + k]->buf.k_cache;
+      a.kv[2 * k + 1] = attns[i + k]->buf.v_cache;
+    }
+    const cudaError_t e = moe::launch_attn_keep(a, h->num_sms, static_cast<cudaStream_t>(stream), h->pdl);
+    if (e != cudaSuccess) return cuda_error(e, fn);
+  }
+  return MOE_OK;
 }
 
 moe_status_t moe_attn_sync(moe_attn_t* h, void* stream) {

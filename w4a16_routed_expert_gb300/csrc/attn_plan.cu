@@ -1,0 +1,307 @@
+// A step's tables (moe_attn_plan): from each sequence's context, new tokens and
+// pages held, three running sums over the sequences (tokens, pages taken, pages
+// given back) say where everything goes:
+//   q_offsets[b] = sum_{b' < b} m_b',   need_b = max(0, ceil((c_b + m_b) / p) - held_b)
+//   table[b][held_b + i] = ring[first + sum_{b' < b} need_b' + i]
+// and a tree's masks are the closure of its parents:
+//   row(i) = bit i | row(parent(i)),   depth(i) = popcount(row(i)) - 1
+// taken by doubling (row |= row(jump), jump = jump(jump)): log2(depth) rounds.
+//
+// A few kilobytes are read and written, so launch and the chain of dependent
+// loads bound it (lengths, then parents or ring, then the stores). One launch:
+// every block takes the sums over all sequences for itself (at most 4096, a few
+// words a thread) instead of waiting for another, and then its share of the
+// sequences, pages and tokens. The pool's state may be updated in place: the
+// last block to end writes it, when none reads it any more.
+#include <algorithm>
+
+#include "attn_dev.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMost = 1 << 30;  // sums stop here
+
+struct SmemPlan {
+  uint32_t off, take, back, served, rows, jump, bytes;
+};
+__host__ __device__ inline SmemPlan smem_plan(int B, int max_nodes, int words) {
+  SmemPlan p;
+  p.off = 0;
+  p.take = p.off + (uint32_t)(B + 1) * 4;
+  p.back = p.take + (uint32_t)(B + 1) * 4;
+  p.served = p.back + (uint32_t)(B + 1) * 4;
+  p.rows = (p.served + (uint32_t)B + 3) & ~3u;
+  const uint32_t nodes = max_nodes > 32 ? (uint32_t)max_nodes : 0u;
+  p.jump = p.rows + nodes * (uint32_t)words * 4;
+  p.bytes = p.jump + 2 * nodes * 4;
+  return p;
+}
+
+__device__ __forceinline__ int add_most(int x, int y) { return min(x + y, kMost); }
+
+// What a sequence asks for.
+struct Ask {
+  int m;     // tokens
+  int need;  // pages beyond those it holds
+  int back;  // pages it gives back
+  bool valid;
+};
+__device__ __forceinline__ Ask ask_of(const PlanArgs& a, int ctx, int fresh, int held) {
+  Ask k;
+  const long long keys = (long long)ctx + max(fresh, 0);
+  k.valid = fresh >= -1 && held >= 0 && held <= a.table_stride &&
+            (fresh < 0 || (ctx >= 0 && keys <= (long long)a.table_stride * a.page_size)) &&
+            (a.max_nodes == 0 || fresh <= a.max_nodes);
+  k.m = min(max(fresh, 0), a.T + 1);
+  k.need = k.valid && fresh >= 0 ? max(0, (int)((keys + a.page_size - 1) / a.page_size) - held) : 0;
+  k.back = k.valid && fresh < 0 ? held : 0;
+  return k;
+}
+
+// The last b with at[b] <= x; at ascends, at[0] = 0.
+__device__ __forceinline__ int find(const int* at, int B, int x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int part[3][kThreads / 32];
+  __shared__ int most_taken, is_last;
+  const SmemPlan sp = smem_plan(a.B, a.max_nodes, a.words);
+  int* off = reinterpret_cast<int*>(smem + sp.off);
+  int* take = reinterpret_cast<int*>(smem + sp.take);
+  int* back = reinterpret_cast<int*>(smem + sp.back);
+  unsigned char* served = smem + sp.served;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.B, F = a.ring_size;
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- the three running sums
+  int first = a.state[0], count = a.state[1];
+  bool bad = first < 0 || first >= F || count < 0 || count > F;
+  first = first < 0 || first >= F ? 0 : first;
+  count = min(max(count, 0), F);
+  const int per = (B + kThreads - 1) / kThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  auto ask = [&](int b) { return ask_of(a, a.context_lens[b], a.new_lens[b], a.state[2 + b]); };
+  int sum[3] = {0, 0, 0};
+  if (tid == 0) most_taken = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const Ask k = ask(b);
+    sum[0] = add_most(sum[0], k.m);
+    sum[1] = add_most(sum[1], k.need);
+    sum[2] = add_most(sum[2], k.back);
+    bad |= !k.valid;
+  }
+  int incl[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    incl[i] = sum[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] = add_most(incl[i], y);
+    }
+    if (lane == 31) part[i][warp] = incl[i];
+  }
+  __syncthreads();
+  int base[3], total[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int y = __shfl_up_sync(0xffffffffu, incl[i], 1);
+    base[i] = lane ? y : 0;
+    total[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base[i] = add_most(base[i], part[i][w]);
+      total[i] = add_most(total[i], part[i][w]);
+    }
+  }
+  int mine = 0;  // pages taken up to this thread's last sequence that is served
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const Ask k = ask(b);
+    off[b] = base[0];
+    take[b] = base[1];
+    back[b] = base[2];
+    const bool room = base[0] + k.m <= a.T;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) base[i] = add_most(base[i], i == 0 ? k.m : i == 1 ? k.need : k.back);
+    const bool ok = k.valid && a.new_lens[b] >= 0 && room && (k.need == 0 || base[1] <= count);
+    served[b] = ok;
+    if (ok && k.need) mine = base[1];
+    bad |= !room;
+  }
+  if (tid == 0) {
+    off[B] = total[0];
+    take[B] = total[1];
+    back[B] = total[2];
+  }
+  if (mine) atomicMax(&most_taken, mine);
+  if (bad && blockIdx.x == 0) record_error(a.err, kAttnErrBounds);
+  __syncthreads();
+  const int taken = most_taken;
+  const int given = min(back[B], F - count);
+  if (given < back[B] && blockIdx.x == 0 && tid == 0) record_error(a.err, kAttnErrBounds);
+
+  const int grid_threads = gridDim.x * kThreads, gtid = blockIdx.x * kThreads + tid;
+  auto ring_at = [&](int i) {  // i < 2 F
+    const int x = first + (i >= F ? i - F : i);
+    return x >= F ? x - F : x;
+  };
+  // ---- per sequence, per page
+  for (int b = gtid; b <= B; b += grid_threads) {
+    a.q_offsets[b] = min(off[b], a.T);
+    if (b < B) a.seq_lens[b] = served[b] ? a.context_lens[b] + a.new_lens[b] : 0;
+  }
+  for (int i = gtid; i < taken; i += grid_threads) {
+    const int b = find(take, B, i);
+    a.block_table[(long long)b * a.table_stride + a.state[2 + b] + i - take[b]] = a.free_pages[ring_at(i)];
+  }
+  for (int i = gtid; i < given; i += grid_threads) {
+    const int b = find(back, B, i);
+    a.free_pages[ring_at(count + i)] = a.block_table[(long long)b * a.table_stride + i - back[b]];
+  }
+
+  // ---- per token
+  // The slot of a sequence's key: its page stands in the table, or is being
+  // taken from the ring by this step.
+  auto slot = [&](int b, int key) {
+    const int held = a.state[2 + b], pg = key / a.page_size;
+    const int page = pg < held ? a.block_table[(long long)b * a.table_stride + pg]
+                               : a.free_pages[ring_at(take[b] + pg - held)];
+    if ((unsigned)page >= (unsigned)a.num_pages) {
+      record_error(a.err, kAttnErrBounds);
+      return -1;
+    }
+    return page * a.page_size + key - pg * a.page_size;
+  };
+  const int tokens = min(off[B], a.T);
+  if (a.max_nodes == 0) {
+    for (int t = gtid; t < tokens; t += grid_threads) {
+      const int b = find(off, B, t), key = a.context_lens[b] + t - off[b];
+      a.positions[t] = a.prefix_len + key;
+      a.slots[t] = served[b] ? slot(b, key) : -1;
+    }
+  } else {
+    auto parent_of = [&](int t, int i) {
+      int p = a.parents[t];
+      if (p < -1 || p >= i) {
+        record_error(a.err, kAttnErrBounds);
+        p = -1;
+      }
+      return p;
+    };
+    auto place = [&](int b, int t, int i, int depth) {
+      const int ctx = a.context_lens[b];
+      a.positions[t] = a.prefix_len + ctx + depth;
+      a.slots[t] = served[b] ? slot(b, ctx + i) : -1;
+    };
+    // trees of up to 32 tokens: a warp each, a lane a token
+    for (int b = blockIdx.x + gridDim.x * warp; b < B; b += gridDim.x * (kThreads / 32)) {
+      const int t0 = min(off[b], a.T), m = min(off[b + 1], a.T) - t0;
+      if (m <= 0 || m > 32) continue;
+      int jump = lane < m ? parent_of(t0 + lane, lane) : -1;
+      uint32_t row = 1u << lane;
+      while (__any_sync(0xffffffffu, jump >= 0)) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, jump & 31);
+        const int j = __shfl_sync(0xffffffffu, jump, jump & 31);
+        if (jump >= 0) {
+          row |= r;
+          jump = j;
+        }
+      }
+      if (lane < m) {
+        place(b, t0 + lane, lane, __popc(row) - 1);
+        uint32_t* out = a.tree + (long long)(t0 + lane) * a.words;
+        out[0] = row;
+        for (int w = 1; w < a.words; ++w) out[w] = 0;
+      }
+    }
+    // larger ones: a block each
+    uint32_t* rows = reinterpret_cast<uint32_t*>(smem + sp.rows);
+    const int W = a.words;
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      const int t0 = min(off[b], a.T), m = min(off[b + 1], a.T) - t0;
+      if (m <= 32) continue;
+      if (m > a.max_nodes) {  // (recorded above)
+        for (int i = tid; i < m * W; i += kThreads) a.tree[(long long)t0 * W + i] = 0;
+        for (int i = tid; i < m; i += kThreads) place(b, t0 + i, i, 0);
+        continue;
+      }
+      int* jump = reinterpret_cast<int*>(smem + sp.jump);
+      int* next = jump + a.max_nodes;
+      __syncthreads();  // the tree before has been read
+      for (int i = tid; i < m; i += kThreads) jump[i] = parent_of(t0 + i, i);
+      for (int i = tid; i < m * W; i += kThreads) rows[i] = i % W == (i / W) >> 5 ? 1u << ((i / W) & 31) : 0u;
+      __syncthreads();
+      // A row may be read while its own thread adds to it: whatever is read holds
+      // at least the branch up to where `jump` stood before the round.
+      while (true) {
+        bool more = false;
+        for (int i = tid; i < m * W; i += kThreads) {
+          const int n = i / W, w = i - n * W, j = jump[n];
+          if (j >= 0) {
+            more = true;
+            const uint32_t r = *(volatile uint32_t*)(rows + j * W + w);
+            *(volatile uint32_t*)(rows + i) |= r;
+          }
+          if (w == 0) next[n] = j >= 0 ? jump[j] : -1;
+        }
+        int* x = jump;
+        jump = next;
+        next = x;
+        if (!__syncthreads_or(more)) break;
+      }
+      for (int i = tid; i < m * W; i += kThreads) a.tree[(long long)t0 * W + i] = rows[i];
+      for (int i = tid; i < m; i += kThreads) {
+        int depth = -1;
+        for (int w = 0; w < W; ++w) depth += __popc(rows[i * W + w]);
+        place(b, t0 + i, i, depth);
+      }
+    }
+    for (long long i = (long long)tokens * a.words + gtid; i < (long long)a.T * a.words; i += grid_threads) a.tree[i] = 0;
+  }
+  for (int t = tokens + gtid; t < a.T; t += grid_threads) {
+    a.positions[t] = 0;
+    a.slots[t] = -1;
+  }
+
+  // ---- the pool's state, when no block reads the old one any more
+  __syncthreads();
+  if (tid == 0) is_last = gridDim.x == 1 || atom_acq_rel_add(a.ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!is_last) return;
+  for (int b = tid; b < B; b += kThreads) {
+    const int held = a.state[2 + b];
+    a.state_out[2 + b] = served[b] ? held + take[b + 1] - take[b] : back[b + 1] > back[b] ? 0 : held;
+  }
+  if (tid == 0) {
+    a.state_out[0] = ring_at(taken);
+    a.state_out[1] = count - taken + given;
+    *a.ticket = 0;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_plan(const PlanArgs& a, int num_sms, cudaStream_t s, bool pdl) {
+  const size_t smem = smem_plan(a.B, a.max_nodes, a.words).bytes;
+  const cudaError_t e = ensure_smem(k_attn_plan, smem);
+  if (e != cudaSuccess) return e;
+  const int by_tokens = (a.T + 1023) / 1024, by_trees = a.max_nodes ? a.B : 0;
+  const int grid = std::max(1, std::min(2 * num_sms, std::max(by_tokens, by_trees)));
+  return launch_ex(k_attn_plan, dim3(grid), dim3(kThreads), smem, s, pdl, a);
+}
+
+}  // namespace moe

@@ -67,7 +67,10 @@ __device__ __forceinline__ bool bar_any(bool v) {
   return any != 0;
 }
 
-template <typename T, int DP, int MT>
+// TREE: a token sees of its sequence's new tokens those that its bits name
+// (AttnArgs::tree); a tile that reaches behind the context takes a word of
+// them a row.
+template <typename T, int DP, int MT, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
     k_attn_rows(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2, int late_wait) {
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (bar_any(!ok) || !some) break;
       float o[MT][DP / 8][4];
       float mref[MT][2], l[MT][2];
-      int lim[MT][2];  // keys each of the lane's rows sees
+      int lim[MT][2];  // keys each of the lane's rows sees; TREE: where its token's bits are
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -259,11 +262,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           mref[m][e] = -INFINITY;
           l[m][e] = 0.f;
           const int row = s.row0 + min(m * 16 + g8 + 8 * e, s.rows - 1);
-          lim[m][e] = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
+          if (TREE)
+            lim[m][e] = (s.t0 + row / a.g) * a.tree_words;
+          else
+            lim[m][e] = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
         }
       }
       // keys that every row sees: no masking needed below it
-      const int all_see = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, s.row0 / a.g);
+      const int all_see = s.b < 0 ? s.klen : TREE ? s.klen - s.n : keys_seen(a, s.klen, s.n, s.row0 / a.g);
 
 #pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
@@ -314,7 +320,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t pf[MT][4], pl[MT][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            if (k0 + 16 > all_see) {
+            if (TREE && k0 + 16 > all_see) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t vis = low_bits(s.klen - k0);
+                if (s.b >= 0) vis &= tree_window(a.tree + lim[m][e], a.tree_words, k0 - all_see);
+                vis >>= t4 * 2;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  if (!((vis >> (n * 8)) & 1u)) sv[m][n][2 * e] = -INFINITY;
+                  if (!((vis >> (n * 8)) & 2u)) sv[m][n][2 * e + 1] = -INFINITY;
+                }
+              }
+            }
+            if (!TREE && k0 + 16 > all_see) {
 #pragma unroll
               for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (late_wait) pdl_wait();  // ends after the kernel before it, so what waits for this one waits for both
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool TREE>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
                    const AttnRowsPlan& p, int box_log2, bool late_wait, cudaStream_t s, bool pdl) {
   auto run = [&](auto kern) {
@@ -509,8 +528,18 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
                      (int)late_wait);
   };
   if constexpr (rows_most(DP) > 16)
-    if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2>);
-  return run(k_attn_rows<T, DP, 1>);
+    if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2, TREE>);
+  return run(k_attn_rows<T, DP, 1, TREE>);
+}
+
+template <typename T>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln,
+                     const AttnRowsPlan& p, int bl, bool late_wait, cudaStream_t s, bool pdl) {
+  if (a.D <= 64)
+    return a.tree ? launch<T, 64, true>(tk, tv, a, ln, p, bl, late_wait, s, pdl)
+                  : launch<T, 64, false>(tk, tv, a, ln, p, bl, late_wait, s, pdl);
+  return a.tree ? launch<T, 128, true>(tk, tv, a, ln, p, bl, late_wait, s, pdl)
+                : launch<T, 128, false>(tk, tv, a, ln, p, bl, late_wait, s, pdl);
 }
 
 }  // namespace
@@ -532,11 +561,8 @@ cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const
                              bool pdl) {
   int bl = 4;
   while ((1 << bl) < box_slots) ++bl;
-  if (a.D <= 64)
-    return bf16 ? launch<__nv_bfloat16, 64>(tk, tv, a, ln, p, bl, late_wait, s, pdl)
-                : launch<__half, 64>(tk, tv, a, ln, p, bl, late_wait, s, pdl);
-  return bf16 ? launch<__nv_bfloat16, 128>(tk, tv, a, ln, p, bl, late_wait, s, pdl)
-              : launch<__half, 128>(tk, tv, a, ln, p, bl, late_wait, s, pdl);
+  return bf16 ? launch_t<__nv_bfloat16>(tk, tv, a, ln, p, bl, late_wait, s, pdl)
+              : launch_t<__half>(tk, tv, a, ln, p, bl, late_wait, s, pdl);
 }
 
 bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int page_size, int Hk, long long num_pages,

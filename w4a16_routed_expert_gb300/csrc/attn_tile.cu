@@ -76,8 +76,10 @@ struct Misc {
 static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 
 // RSUM: the quotient takes the sum of the weights as they were rounded for the
-// products (few rows, see launch_attn_tile).
-template <typename T, int DP, bool RSUM>
+// products (few rows, see launch_attn_tile). TREE: a token sees of its
+// sequence's new tokens those that its bits name (AttnArgs::tree); a tile that
+// reaches behind the context takes four words of them a row.
+template <typename T, int DP, bool RSUM, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2) {
@@ -502,8 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 l2 = make_float2(0.f, 0.f), lr2 = l2;
       if (used) {
         const int row = cur->row0 + min(r, cur->rows - 1);
-        const int lim = cur->b < 0 ? cur->klen : keys_seen(a, cur->klen, cur->n, row / a.g);
-        const int all_see = cur->b < 0 ? cur->klen : keys_seen(a, cur->klen, cur->n, cur->row0 / a.g);
+        const int lim = TREE || cur->b < 0 ? cur->klen : keys_seen(a, cur->klen, cur->n, row / a.g);
+        const int all_see = cur->b < 0 ? cur->klen
+                            : TREE     ? cur->klen - cur->n
+                                       : keys_seen(a, cur->klen, cur->n, cur->row0 / a.g);
+        const uint32_t* bits = TREE && cur->b >= 0 ? a.tree + (long long)(cur->t0 + row / a.g) * a.tree_words : nullptr;
         const int tile0 = cur->tile, front = cur->front, nkeys = cur->nkeys;
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
@@ -538,8 +543,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             // reference moved to the maximum and the tile, still in tensor
             // memory, done again: once, after which no weight passes 2^bias.
             // The first tile sets it beforehand.
+            uint32_t vis[4];  // TREE: the tile's keys that the row sees
+            bool sees = k0 < seen;
+            if (TREE && edge) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                vis[c] = low_bits(seen - k0 - c * 32);
+                if (bits && !pre) vis[c] &= tree_window(bits, a.tree_words, k0 + c * 32 - all_see);
+              }
+              sees = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
+            }
             auto mask = [&](uint32_t(&v)[32], int c) {
-              if (edge) {
+              if (TREE) {
+                if (edge) {
+                  const uint32_t w = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!((w >> e) & 1u)) v[e] = 0xff800000u;
+                }
+              } else if (edge) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if (k0 + c * 32 + e >= seen) v[e] = 0xff800000u;
@@ -611,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < 3) tmem_ld_wait_for(sr[(c + 1) & 1]);
               }
               if (move) break;
-              move = __any_sync(0xffffffffu, lt.x + lt.y > kSumMost || (mref == -INFINITY && k0 < seen));
+              move = __any_sync(0xffffffffu, lt.x + lt.y > kSumMost || (mref == -INFINITY && sees));
               if (!move) break;
             }
             l2 = fadd2(l2, lt);
@@ -738,15 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP, bool RSUM>
+template <typename T, int DP, bool RSUM, bool TREE>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
                    cudaStream_t s, bool pdl) {
   int stages = kMaxStages;  // as many as fit
   while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
   const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
-  const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM>, smem);
+  const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE>, smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k_attn_tile<T, DP, RSUM>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
+  return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
                    box_log2);
 }
 
@@ -756,13 +778,15 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
 // hundred keys, up to 1.8 times, or 1.4 with the quotient by the rounded sum,
 // which costs about 10% (four chunks of 770 tokens 406 us against 370, 64
 // sequences behind 32768 keys 92 against 83). Below 4096 rows it is taken.
-template <typename T>
+template <typename T, bool TREE>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int bl,
                      cudaStream_t s, bool pdl) {
   const bool few = (long long)a.T * a.Hq < 4096;
   if (a.D <= 64)
-    return few ? launch<T, 64, true>(tk, tv, a, ln, bl, s, pdl) : launch<T, 64, false>(tk, tv, a, ln, bl, s, pdl);
-  return few ? launch<T, 128, true>(tk, tv, a, ln, bl, s, pdl) : launch<T, 128, false>(tk, tv, a, ln, bl, s, pdl);
+    return few ? launch<T, 64, true, TREE>(tk, tv, a, ln, bl, s, pdl)
+               : launch<T, 64, false, TREE>(tk, tv, a, ln, bl, s, pdl);
+  return few ? launch<T, 128, true, TREE>(tk, tv, a, ln, bl, s, pdl)
+             : launch<T, 128, false, TREE>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace
@@ -771,7 +795,11 @@ cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const
                              int box_slots, bool bf16, cudaStream_t s, bool pdl) {
   int bl = 4;
   while ((1 << bl) < box_slots) ++bl;
-  return bf16 ? launch_t<__nv_bfloat16>(tk, tv, a, ln, bl, s, pdl) : launch_t<__half>(tk, tv, a, ln, bl, s, pdl);
+  if (a.tree)
+    return bf16 ? launch_t<__nv_bfloat16, true>(tk, tv, a, ln, bl, s, pdl)
+                : launch_t<__half, true>(tk, tv, a, ln, bl, s, pdl);
+  return bf16 ? launch_t<__nv_bfloat16, false>(tk, tv, a, ln, bl, s, pdl)
+              : launch_t<__half, false>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace moe
