@@ -113,8 +113,12 @@ bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int 
 // beside a second block (20 rows of 128 over 16 sequences of 8000 keys: 173 us,
 // 138 with one block an SM, 95 on the tcgen05 tiles; at 64, 20 rows behind 8192
 // keys: 23 us, 29 on the tcgen05 tiles).
-constexpr int kRowsMax = 32;
-constexpr int rows_most(int D) { return D <= 64 ? kRowsMax : 16; }
+// Over trees up to 64 and 32, the warps as 1 by 4, 2 by 2 or 4 by 1 groups of 16
+// rows and of keys (50 trees of up to 52 rows of 64 with up to 713 keys: 30 us,
+// 42 on the tcgen05 tiles; 16 of up to 31 rows of 128 with up to 2600 keys: 44
+// and 51; but 64 rows of 128 over 8 sequences of 15000 keys: 156 and 85).
+constexpr int kRowsMax = 64;
+constexpr int rows_most(int D, bool tree) { return tree ? (D <= 64 ? 64 : 32) : D <= 64 ? 32 : 16; }
 // (query token, query head, prefix key) triples up to which it takes the
 // prefix's rows beside few own rows, however many. In its launch / in one of
 // the tcgen05 kernel before it, own keys to 200: 24 rows of 128 over 300, 4000,
@@ -124,10 +128,10 @@ constexpr int rows_most(int D) { return D <= 64 ? kRowsMax : 16; }
 constexpr long long kFewTriples = 1LL << 22;
 constexpr int kRowsKeyTile = 64;
 struct AttnRowsPlan {
-  int n_cta, stages;
+  int n_cta, stages, row_groups;
   size_t smem;
 };
-AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms);
+AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms, bool tree);
 // LineArgs::weight (0, 1, 2, 3, 5 for 16 sequences behind 4099 keys: 36.4, 26.1,
 // 26.0, 26.1, 26.9 us; for 48 sequences of drafts: 59.5, 50.5, 47.7, 48.1, 48.5)
 constexpr int kRowsWeight = 2;

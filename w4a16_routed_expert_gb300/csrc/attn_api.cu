@@ -196,7 +196,8 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
   // kernel, of which a block takes two. Beside few own rows a prefix of many
   // stays in the few-row kernel's launch while there is little to compute, in
   // row blocks that read its keys once each.
-  const int most = moe::rows_most(a.D);
+  const bool over_tree = a.tree != nullptr;
+  const int most = moe::rows_most(a.D, over_tree);
   const bool little = own_rows && (long long)a.T * a.Hq * a.prefix_len <= moe::kFewTriples;
   const bool tile_own = own_rows > most;
   const bool tile_prefix = prefix_rows && (tile_own || (prefix_rows > most && !little));
@@ -244,8 +245,8 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
     fits = line(&tile, moe::kTileRows, moe::kTileKeyTile, moe::kTileWeight, h->num_sms, tile_prefix, tile_own);
   if (few_own || few_prefix) {
     const int rows = std::max(few_own ? own_rows : 0, few_prefix ? prefix_rows : 0);
-    const int block = rows <= 16 ? 16 : most;
-    plan = moe::plan_attn_rows(a.D, std::min(rows, block), a.B, h->num_sms);
+    const int block = rows <= 16 ? 16 : over_tree && rows <= 32 ? 32 : most;
+    plan = moe::plan_attn_rows(a.D, std::min(rows, block), a.B, h->num_sms, over_tree);
     fits = line(&few, block, moe::kRowsKeyTile, moe::kRowsWeight, plan.n_cta, few_prefix,
                 few_own) && fits;
   }

@@ -37,11 +37,11 @@ constexpr int kMaxStages = 4;
 struct SmemPlan {
   uint32_t q, merge, ml, bars, seg, misc, off, bytes;
 };
-__host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int rows, int stages, int B) {
+__host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int WR, int rows, int stages, int B) {
   SmemPlan p;
   p.q = (uint32_t)stages * 2 * kKT * DP * 2;
-  p.merge = p.q + (uint32_t)MT * 16 * DP * 2;
-  p.ml = p.merge + 2u * MT * (rows > 8 ? 16 : 8) * DP * 4;
+  p.merge = p.q + (uint32_t)WR * MT * 16 * DP * 2;
+  p.ml = p.merge + (WR == 4 ? 0u : 2u * MT * (rows > 8 ? 16 : 8) * DP * 4);
   p.bars = p.ml + (uint32_t)kWarps * MT * 16 * 8;
   p.seg = p.bars + 2 * (kMaxStages + kSegSlots) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
@@ -67,16 +67,19 @@ __device__ __forceinline__ bool bar_any(bool v) {
   return any != 0;
 }
 
-// TREE: a token sees of its sequence's new tokens those that its bits name
+// WR: the computing warps are WR row groups of 16 MT rows by 4 / WR key groups;
+// a row group's warps share the 64 keys of a stage, 16 at a time. TREE: a token sees of its sequence's new tokens those that its bits name
 // (AttnArgs::tree); a tile that reaches behind the context takes a word of
 // them a row.
-template <typename T, int DP, int MT, bool TREE>
+template <typename T, int DP, int MT, int WR, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
     k_attn_rows(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2, int late_wait) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const SmemPlan sp = smem_plan(DP, MT, ln.part_rows, stages, a.B);
+  constexpr int WK = kWarps / WR;      // key groups
+  constexpr int RB = WR * MT * 16;     // rows of a group at most
+  const SmemPlan sp = smem_plan(DP, MT, WR, ln.part_rows, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
   uint64_t* seg_full = empty + kMaxStages;
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   pdl_trigger();
   if (!late_wait) pdl_wait();
-  const int own_total = scan_own<kThreads, kKT, MT * 16>(a, ln, own_off, scratch);
+  const int own_total = scan_own<kThreads, kKT, RB>(a, ln, own_off, scratch);
   if (!ln.has_own) __syncthreads();
   const int box = 1 << box_log2;
 
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t ph = 0, sph = 0;
     int issued = 0;
     bool ok = true;
-    Walk<kKT, MT * 16> w;
+    Walk<kKT, RB> w;
     w.init(a, ln, own_off, own_total);
     while (ok) {
       Segment s;
@@ -193,8 +196,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ compute
     const int g8 = lane >> 2, t4 = lane & 3;
     const float sc = a.scale * kLog2e;
-    // shared-memory address parts of this warp's 16 keys (all in one box)
-    const uint32_t warp_off = (uint32_t)((warp * 16) >> box_log2) * box * DP * 2 + (uint32_t)((warp * 16) & (box - 1)) * 128;
+    const int wr = warp / WK, wk = warp % WK;  // row group, key group
+    // shared-memory address of 16 of the stage's keys (all in one box)
+    auto keys_off = [&](int key) {
+      return (uint32_t)(key >> box_log2) * box * DP * 2 + (uint32_t)(key & (box - 1)) * 128;
+    };
     const uint32_t half_step = (uint32_t)box * 128;
     const int krow = (lane & 7) + ((lane >> 4) << 3), ksel = (lane >> 3) & 1;
     const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vsel = lane >> 4;
@@ -219,17 +225,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     // queries: rows of 128-byte halves, swizzled as the boxes are; zeros
     // beyond the group's rows and the head's elements
-    constexpr int kQ = MT * 16 * DP / 8 / (kWarps * 32);  // 16-byte words of a thread
-    uint4 qv[kQ] = {};
+    constexpr int kQ = RB * DP / 8 / (kWarps * 32);  // 16-byte words of a thread
+    constexpr bool kAsyncQ = WR > 1;  // by asynchronous copies, once no warp reads the last ones (in registers they spill)
+    uint4 qv[kAsyncQ ? 1 : kQ] = {};
+    auto q_place = [&](int r, int c8) {
+      return sp.q + (uint32_t)(c8 >> 3) * RB * 128 + (uint32_t)r * 128 + (uint32_t)(((c8 & 7) ^ (r & 7)) << 4);
+    };
     auto load_q = [&](const Segment& s) {
 #pragma unroll
       for (int i = 0; i < kQ; ++i) {
         const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
-        qv[i] = make_uint4(0, 0, 0, 0);
-        if (r < s.rows && c8 * 8 < a.D) {
-          const int row = s.row0 + r, tok = row / a.g, hq = s.h * a.g + row - tok * a.g;
-          qv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.t0 + tok) * a.q_stride +
-                                                  (long long)hq * a.D + c8 * 8);
+        const bool valid = r < s.rows && c8 * 8 < a.D;
+        const int row = s.row0 + r, tok = row / a.g, hq = s.h * a.g + row - tok * a.g;
+        const T* src = static_cast<const T*>(a.q) + (long long)(s.t0 + tok) * a.q_stride + (long long)hq * a.D + c8 * 8;
+        if (kAsyncQ) {
+          cp_async16(smem_u32(smem) + q_place(r, c8), valid ? (const void*)src : a.q, valid);
+        } else {
+          qv[kAsyncQ ? 0 : i] = make_uint4(0, 0, 0, 0);
+          if (valid) qv[kAsyncQ ? 0 : i] = *reinterpret_cast<const uint4*>(src);
         }
       }
     };
@@ -241,11 +254,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     // others, and all of them end at the next part's first one. (After the
     // last part the words stored before it are nobody's.)
     while (true) {
+      if (kAsyncQ) {
+        cp_async_wait_all();
+      } else {
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
-        *reinterpret_cast<uint4*>(smem + sp.q + (uint32_t)(c8 >> 3) * MT * 16 * 128 + (uint32_t)r * 128 +
-                                  (uint32_t)(((c8 & 7) ^ (r & 7)) << 4)) = qv[i];
+        for (int i = 0; i < kQ; ++i) {
+          const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
+          *reinterpret_cast<uint4*>(smem + q_place(r, c8)) = qv[kAsyncQ ? 0 : i];
+        }
       }
       if (bar_any(!ok) || !some) break;
       float o[MT][DP / 8][4];
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 2; ++e) {
           mref[m][e] = -INFINITY;
           l[m][e] = 0.f;
-          const int row = s.row0 + min(m * 16 + g8 + 8 * e, s.rows - 1);
+          const int row = s.row0 + min((wr * MT + m) * 16 + g8 + 8 * e, s.rows - 1);
           if (TREE)
             lim[m][e] = (s.t0 + row / a.g) * a.tree_words;
           else
@@ -273,13 +289,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 #pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
-        const int k0 = (s.tile + i) * kKT + warp * 16;
         const bool got = mbar_wait(&full[st], ph, abort_flag, a.err);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        const uint32_t kb = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes + warp_off;
+#pragma unroll 1
+        for (int sub = 0; sub < WR && (WR == 1 || wr * MT * 16 < s.rows); ++sub) {
+        const int key = (wk * WR + sub) * 16, k0 = (s.tile + i) * kKT + key;
+        const uint32_t kb = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes + keys_off(key);
         const uint32_t vb = kb + kTileBytes;
         const int here = s.nkeys - k0;  // keys of this warp's sixteen that exist
         if (here > 0) {
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
               uint32_t qf[4];
-              ldsm4(qs + (uint32_t)(kk >> 2) * MT * 16 * 128 + (uint32_t)(m * 16 + qrow) * 128 +
+              ldsm4(qs + (uint32_t)(kk >> 2) * RB * 128 + (uint32_t)((wr * MT + m) * 16 + qrow) * 128 +
                         (uint32_t)(((c16 + qsel) ^ (qrow & 7)) << 4),
                     qf);
               mma16816<T>(sv[m][0], qf, kf[0], kf[1]);
@@ -403,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (here < 16) fence_async_smem();  // the zeros before the stage's next copies
         }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
         if (++st == stages) {
@@ -413,12 +432,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       // the next part's queries are on their way while this one is joined
       const Segment cur = s;
       some = ok && next_segment(&s);
-      if (some) load_q(s);
+      if (!kAsyncQ && some) load_q(s);
 
       // ---- the four warps' results become one: a common maximum, then the
-      // rescaled sums and output tiles added in a fixed order (3 into 1, 2
-      // into 0, 1 into 0)
-      const int r0 = warp * MT * 16;
+      // rescaled sums and output tiles added in a fixed order (key groups 3 into
+      // 1, 2 into 0, 1 into 0)
+      const int r0 = wk * RB + wr * MT * 16;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -428,18 +447,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (t4 == 0) ml[r0 + m * 16 + g8 + 8 * e] = make_float2(mref[m][e], l[m][e]);
         }
       bar_compute();
+      if (kAsyncQ && some) load_q(s);
       float mt[MT][2], lt[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = m * 16 + g8 + 8 * e;
+          const int r = (wr * MT + m) * 16 + g8 + 8 * e;
           float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * MT * 16 + r].x);
+          for (int w = 0; w < WK; ++w) mm = fmaxf(mm, ml[w * RB + r].x);
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 v = ml[w * MT * 16 + r];
+          for (int w = 0; w < WK; ++w) {
+            const float2 v = ml[w * RB + r];
             ll += v.y * (v.x == mm ? 1.f : exp2_fast((v.x - mm) * sc));
           }
           mt[m][e] = mm;
@@ -453,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       // [slot][row half of 8][tile, column block][lane]
       const int halves = ln.part_rows > 8 ? 2 : 1;
-      float2* buf = reinterpret_cast<float2*>(merge) + (warp & 1) * (halves * MT * (DP / 8) * 32) + lane;
+      float2* buf = reinterpret_cast<float2*>(merge) + (WK == 4 ? wk & 1 : wr) * (halves * MT * (DP / 8) * 32) + lane;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (warp >= 2 && e < halves) {
+        if (wk >= 2 && e < halves) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -466,26 +486,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       bar_compute();
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (warp < 2 && e < halves) {
+        if (WK > 1 && (WK == 4 ? wk < 2 : wk == 1) && e < halves) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < DP / 8; ++n) {
               float2* at = buf + ((e * MT + m) * (DP / 8) + n) * 32;
-              const float2 v = *at;
+              const float2 v = WK == 4 ? *at : make_float2(0.f, 0.f);
               o[m][n][2 * e] += v.x;
               o[m][n][2 * e + 1] += v.y;
-              if (warp == 1) *at = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
+              if (wk == 1) *at = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
             }
         }
       bar_compute();
-      if (warp == 0) {
-        const float2* src = reinterpret_cast<const float2*>(merge) + halves * MT * (DP / 8) * 32 + lane;
+      if (wk == 0) {
+        const float2* src = reinterpret_cast<const float2*>(merge) + (WK == 4 ? 1 : wr) * halves * MT * (DP / 8) * 32 + lane;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int r = m * 16 + g8 + 8 * e;
+            const int r = (wr * MT + m) * 16 + g8 + 8 * e;
             if (r < cur.rows) {
               const bool done = whole(ln, cur);
               const int2 at = cur.parts ? row_place(a, cur, r) : make_int2(0, 0);
@@ -494,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D + t4 * 2;
 #pragma unroll
               for (int n = 0; n < DP / 8; ++n) {
-                const float2 v = src[((e * MT + m) * (DP / 8) + n) * 32];
+                const float2 v = WK > 1 ? src[((e * MT + m) * (DP / 8) + n) * 32] : make_float2(0.f, 0.f);
                 const float2 w = make_float2(o[m][n][2 * e] + v.x, o[m][n][2 * e + 1] + v.y);
                 if (!done)
                   *reinterpret_cast<float2*>(dst + n * 8) = w;
@@ -512,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
       }
       // the buffers are free again once the next part's queries are in
-      // (its first barrier comes after warp 0's reads)
+      // (its first barrier comes after these reads)
     }
   }
   if (late_wait) pdl_wait();  // ends after the kernel before it, so what waits for this one waits for both
@@ -527,9 +547,13 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
     return launch_ex(kern, dim3(p.n_cta), dim3(kThreads), p.smem, s, pdl, tk, tv, a, ln, p.stages, box_log2,
                      (int)late_wait);
   };
-  if constexpr (rows_most(DP) > 16)
-    if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2, TREE>);
-  return run(k_attn_rows<T, DP, 1, TREE>);
+  if constexpr (TREE) {
+    if (p.row_groups == 4) return run(k_attn_rows<T, DP, 1, 4, true>);
+    if (p.row_groups == 2) return run(k_attn_rows<T, DP, 1, 2, true>);
+  } else if constexpr (rows_most(DP, false) > 16) {
+    if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2, 1, false>);
+  }
+  return run(k_attn_rows<T, DP, 1, 1, TREE>);
 }
 
 template <typename T>
@@ -544,14 +568,15 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArg
 
 }  // namespace
 
-AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms) {
-  const int DP = D <= 64 ? 64 : 128, MT = rows <= 16 ? 1 : 2;
+AttnRowsPlan plan_attn_rows(int D, int rows, int B, int num_sms, bool tree) {
+  const int DP = D <= 64 ? 64 : 128, MT = tree || rows <= 16 ? 1 : 2;
   AttnRowsPlan p;
+  const int WR = p.row_groups = !tree || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   // as many stages as let two blocks share an SM (228 KB, 1 KB of it kept per
   // block, and up to 1 KB to align the ring)
   for (p.stages = kMaxStages; p.stages > 2; --p.stages)
-    if (smem_plan(DP, MT, rows, p.stages, B).bytes + 2048 <= 114 * 1024) break;
-  p.smem = smem_plan(DP, MT, rows, p.stages, B).bytes + 1024;
+    if (smem_plan(DP, MT, WR, rows, p.stages, B).bytes + 2048 <= 114 * 1024) break;
+  p.smem = smem_plan(DP, MT, WR, rows, p.stages, B).bytes + 1024;
   p.n_cta = num_sms * (p.smem + 1024 <= 114 * 1024 ? 2 : 1);
   return p;
 }

@@ -53,13 +53,14 @@ constexpr int kMaxStages = 8;
 constexpr float kSumMost = 32768.f;
 
 struct SmemPlan {
-  uint32_t ring, bars, seg, misc, off, bytes;
+  uint32_t ring, ml, bars, seg, misc, off, bytes;
 };
-__host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
+__host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B, bool tree) {
   SmemPlan p;
   p.ring = 2u * 128 * DP * 2;  // after the queries
-  p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
-  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 16) * 8;
+  p.ml = p.ring + (uint32_t)stages * kKT * DP * 2;
+  p.bars = p.ml + (tree ? 128u * 16u : 0u);
+  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 18) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 80;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
@@ -79,6 +80,13 @@ static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 // products (few rows, see launch_attn_tile). TREE: a token sees of its
 // sequence's new tokens those that its bits name (AttnArgs::tree); a tile that
 // reaches behind the context takes four words of them a row.
+//
+// TREE also takes the key tiles of a part with one row tile in two streams, tile
+// j in stream j mod 2 (`dual`): both S and O tiles hold the same rows, so that
+// one stream's products run under the other's softmax as they do for two row
+// tiles, and the streams' sums are joined where the part ends. Trees mostly have
+// such parts (8 sequences of 15000 keys, 64 key rows of 128: 85 us, 91 with one
+// stream; 32 rows: 84 and 106).
 template <typename T, int DP, bool RSUM, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
@@ -95,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kOut = kAhead ? 384 : 256;     // columns of the output tiles
   constexpr uint32_t kHalf = 128 * 128;             // bytes of 64 elements of 128 rows
   constexpr uint32_t kTileBytes = NH * kHalf;       // a query, key or value tile
-  const SmemPlan sp = smem_plan(DP, stages, a.B);
+  const SmemPlan sp = smem_plan(DP, stages, a.B, TREE);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
   uint64_t* q_full = empty + kMaxStages;  // [2] queries in shared memory and the output tile drained
@@ -108,6 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_full = o_full + 4;
   uint64_t* seg_empty = seg_full + kSegSlots;
   uint64_t* drain = seg_empty + kSegSlots;
+  uint64_t* d_full = drain + 1;   // both streams' output complete
+  uint64_t* ml_full = d_full + 1; // the second stream's maxima and sums in shared memory
   Segment* segs = reinterpret_cast<Segment*>(smem + sp.seg);
   Misc* misc = reinterpret_cast<Misc*>(smem + sp.misc);
   int32_t* own_off = reinterpret_cast<int32_t*>(smem + sp.off);
@@ -132,6 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&seg_empty[i], 10);  // eight softmax warps, kWarpMma, kWarpLanded
     }
     mbar_init(drain, 1);
+    mbar_init(d_full, 1);
+    mbar_init(ml_full, 4);
     misc->abort_flag = 0;
     misc->issued = 0;
     misc->mma_issued = 0;
@@ -151,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc->tmem;
+  auto is_dual = [](const Segment& s) { return TREE && s.rows <= 128 && s.tiles > 1; };
 
   if (warp >= kWarpCopy) {
   if (warp == kWarpCopy) {
@@ -202,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1u;
         }
       };
-      // keys and values in turn, with kAhead the next tile's keys before a
+      // keys and values in turn, with kAhead or two streams the next tile's keys before a
       // tile's values: the order in which the MMA warp comes to them
       int page = page_of(s.tile);
       // (the first page's number is on its way meanwhile)
@@ -219,13 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!some) break;
       int vpage = 0, vat = 0, vboxes = 0;
       bool vhave = false;
+      const bool ahead = kAhead || is_dual(s);
 #pragma unroll 1
-      for (int i = 0; i < s.tiles + (kAhead ? 1 : 0) && ok; ++i) {
+      for (int i = 0; i < s.tiles + (ahead ? 1 : 0) && ok; ++i) {
         const int at = slot, boxes = (here + box - 1) >> box_log2;
         const bool has = have;
         const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : 0;
         if (i < s.tiles) issue(&tk, has, page, at, boxes);
-        if (!kAhead) {
+        if (!ahead) {
           if (ok) issue(&tv, has, page, at, boxes);
         } else {
           if (ok && i > 0) issue(&tv, vhave, vpage, vat, vboxes);
@@ -263,36 +277,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto place = [&](int t, int j) { return (uint32_t)(kAhead ? (2 * j + t) % 3 : t) * 128; };
       auto bar = [&](int t, int j) { return 2 * t + (kAhead ? j & 1 : 0); };
-      auto qk = [&](int t, int j, int stage) {
-        const uint64_t q = dq + (uint64_t)(t * (kTileBytes >> 4)), k0 = dk + (uint64_t)(stage * (kTileBytes >> 4));
-        const uint32_t d = tm + place(t, j);
+      auto qk_at = [&](int qt, int i, uint32_t d, int stage) {
+        const uint64_t q = dq + (uint64_t)(qt * (kTileBytes >> 4)), k0 = dk + (uint64_t)(stage * (kTileBytes >> 4));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint64_t off = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
           mma_ss(elect, d, q + off, k0 + off, id_s, k > 0);
         }
-        commit_elect(elect, &s_full[bar(t, j)]);
+        commit_elect(elect, &s_full[i]);
       };
+      auto qk = [&](int t, int j, int stage) { qk_at(t, bar(t, j), tm + place(t, j), stage); };
       // waits for the probabilities of (t, j) in tensor memory, and with them
       // (kWarpLanded) for what the products up to the next wait read
-      auto pv = [&](int t, int j, int stage) {
-        const int i = bar(t, j);
+      auto pv_at = [&](int t, int i, uint32_t p, int stage, bool first) {
         if (!wait(&p_full[i], pph[i])) return false;
         pph[i] ^= 1u;
         tc_fence_after();
         const uint64_t v0 = dv + (uint64_t)(stage * (kTileBytes >> 4));
-        const uint32_t d = tm + kOut + t * DP, p = tm + place(t, j);
+        const uint32_t d = tm + kOut + t * DP;
 #pragma unroll
         for (int k = 0; k < kKT / 16; ++k)
-          mma_ts(elect, d, p + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o, (j > 0 || k > 0) ? 1u : 0u);
+          mma_ts(elect, d, p + k * 8, v0 + (uint64_t)(k * (2048 >> 4)), id_o, (!first || k > 0) ? 1u : 0u);
         return true;
       };
+      auto pv = [&](int t, int j, int stage) { return pv_at(t, bar(t, j), tm + place(t, j), stage, j == 0); };
       bool ok = true;
       while (ok) {
         ok = wait(&seg_full[slot_i], sph);
         if (!ok) break;
         const int tiles = __shfl_sync(0xffffffffu, segs[slot_i].tiles, 0);
         const int nt = __shfl_sync(0xffffffffu, segs[slot_i].rows, 0) > 128 ? 2 : 1;
+        const bool dual = TREE && nt == 1 && tiles > 1;
         __syncwarp();
         if (elect) mbar_arrive(&seg_empty[slot_i]);
         if (++slot_i == kSegSlots) {
@@ -312,7 +327,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         commit_elect(elect, &empty[st]);
         step();
-        if (!kAhead) {
+        if (dual) {
+          // stream t: S and P in columns t * 128, as barriers those of row tile t
+          // with an even key tile; the queries are row tile 0's
+          ok = wait(&full[st], ph);
+          if (!ok) break;
+          tc_fence_after();
+          qk_at(0, 2, tm + 128, st);
+          commit_elect(elect, &empty[st]);
+          step();
+#pragma unroll 1
+          for (int i = 0; i < tiles; ++i) {
+            const int t = i & 1, vst = st;
+            step();
+            ok = pv_at(t, 2 * t, tm + t * 128, vst, i < 2);
+            if (!ok) break;
+            commit_elect(elect, &empty[vst]);
+            if (i + 2 < tiles) {
+              qk_at(0, 2 * t, tm + t * 128, st);
+              commit_elect(elect, &empty[st]);
+              step();
+            }
+          }
+          if (ok) commit_elect(elect, d_full);
+        } else if (!kAhead) {
 #pragma unroll 1
           for (int i = 0; i < tiles && ok; ++i) {
             const int vst = st;
@@ -391,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&seg_full[slot_i], sph);
       if (!ok) break;
       const int tiles = segs[slot_i].tiles, nt = segs[slot_i].rows > 128 ? 2 : 1;
+      const bool dual = is_dual(segs[slot_i]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[slot_i]);
       if (++slot_i == kSegSlots) {
@@ -399,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tiles == 0) break;
       auto join = [&](int t, int j) {
-        const int i = 2 * t + (kAhead ? j & 1 : 0);
+        const int i = 2 * t + (kAhead && !dual ? j & 1 : 0);
         if (!wait(&p_full[i], pph[i])) return false;  // the phase before is over: this arrival counts for the next
         pph[i] ^= 1u;
         if (lane == 0) mbar_arrive(&p_full[i]);
@@ -407,10 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // behind P V of (t, i) the MMA warp goes on to the Q K^T of (t, i + 1), or
       // with kAhead of the other row tile's next key tile
-      ok = landed() && (!kAhead || tiles == 1 || landed());
+      ok = landed() && ((!kAhead && !dual) || tiles == 1 || landed());
 #pragma unroll 1
       for (int i = 0; i < tiles && ok; ++i) {
-        if (!kAhead) {
+        if (dual) {  // behind P V of tile i comes the Q K^T of its stream's next
+          ok = landed() && (i + 2 >= tiles || landed()) && join(i & 1, i);
+        } else if (!kAhead) {
           ok = landed() && (i + 1 == tiles || landed());
           for (int t = 0; t < nt && ok; ++t) ok = join(t, i);
         } else {
@@ -425,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;                       // row tile
-    const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the group
+    const int r_lane = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lanes + kOut + t * DP;
     const float sc = a.scale * kLog2e;
@@ -433,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // queries of this row tile, 16 bytes a thread, consecutive threads along a
     // row: asynchronous copies, complete after cp_async_wait_all; zeros beyond
     // the group's rows and the head's elements
-    auto load_q = [&](const Segment* s) {
+    auto load_q = [&](const Segment* s, int t) {
       constexpr int kStep = 128 / (DP / 8);  // rows the 128 threads cover
       const int z = tid & 127, c8 = z & (DP / 8 - 1);
       const int step_tok = kStep / a.g, step_head = kStep - step_tok * a.g;
@@ -477,7 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         gph ^= 1u;
       }
     };
-    auto uses = [&](const Segment* s) { return t == 0 || s->rows > 128; };
+    auto uses = [&](const Segment* s) { return t == 0 || s->rows > 128 || is_dual(*s); };
+    float4* ml = reinterpret_cast<float4*>(smem + sp.ml);
+    uint32_t dph = 0;  // d_full, ml_full
     auto q_arrive = [&]() {
       cp_async_wait_all();
       fence_async_smem();
@@ -486,17 +529,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, some = peek_segment();
     const Segment* cur = &segs[slot_i];
     if (some) {
-      if (uses(cur)) {
-        load_q(cur);
+      if (t == 0 || cur->rows > 128) {
+        load_q(cur, t);
         q_arrive();
       }
       next_slot();
     }
     while (some) {
-      const bool used = uses(cur);
-      bool more = false, more_used = false;  // there is another part, and this row tile has rows in it
-      const bool any_row = t * 128 + (warp & 3) * 32 < cur->rows;
-      const int tiles = cur->tiles;  // this warp has a row
+      const bool used = uses(cur), dual = is_dual(*cur);
+      bool more = false, more_q = false;  // there is another part, and this row tile has queries in it
+      const int r = (dual ? 0 : t * 128) + r_lane;  // row of the group
+      const bool any_row = r - lane < cur->rows;    // this warp has a row
+      const int tiles = cur->tiles;
+      // Once a part's last Q K^T has completed the next one's queries may come in
+      // under its softmax: each row tile's by its own warps, after two streams
+      // the first's by those that have the last key tile.
+      auto next_queries = [&](bool last) {
+        more = peek_segment();
+        const Segment* n = &segs[slot_i];
+        more_q = more && (t == 0 || n->rows > 128);
+        if (more && (dual ? last : t == 0)) load_q(n, 0);
+        if (more_q && t == 1) load_q(n, 1);
+      };
       float mref = -INFINITY;
       // sums of the weights, and (RSUM) of the weights as rounded: the quotient
       // takes the latter, so that a key that stands alone gives its value
@@ -511,12 +565,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t* bits = TREE && cur->b >= 0 ? a.tree + (long long)(cur->t0 + row / a.g) * a.tree_words : nullptr;
         const int tile0 = cur->tile, front = cur->front, nkeys = cur->nkeys;
 #pragma unroll 1
-        for (int i = 0; i < tiles; ++i) {
+        for (int i = dual ? t : 0; i < tiles; i += dual ? 2 : 1) {
           const bool pre = tile0 + i < front;  // a tile of the prefix before own keys
+          const bool first = dual ? i < 2 : i == 0;
           const int k0 = (tile0 + i - (pre ? 0 : front)) * kKT;
           const int nk = pre ? a.prefix_len : nkeys;
-          const int par = kAhead ? i & 1 : 0;
-          const uint32_t ts = tmem + lanes + (uint32_t)(kAhead ? (2 * i + t) % 3 : t) * 128;
+          const int par = kAhead && !dual ? i & 1 : 0;
+          const uint32_t ts = tmem + lanes + (uint32_t)(kAhead && !dual ? (2 * i + t) % 3 : t) * 128;
+          const bool edge = k0 + kKT > (pre ? a.prefix_len : all_see);
+          const int seen = pre ? a.prefix_len : lim;
+          uint32_t vis[4];  // TREE: the tile's keys that the row sees
+          bool sees = k0 < seen;
+          if (TREE && edge) {  // (asked for before the wait)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vis[c] = low_bits(seen - k0 - c * 32);
+            if (bits && !pre) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) vis[c] &= tree_window(bits, a.tree_words, k0 + c * 32 - all_see);
+            }
+            sees = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
+          }
           const bool got = mbar_wait(&s_full[2 * t + par], sph[par], abort_flag, a.err);
           sph[par] ^= 1u;
           if (!__all_sync(0xffffffffu, got)) {
@@ -524,16 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (i + 1 == tiles) {
-            // this part's last Q K^T has completed: the next one's queries may
-            // come in under its softmax
-            more = peek_segment();
-            more_used = more && uses(&segs[slot_i]);
-            if (more_used) load_q(&segs[slot_i]);
-          }
+          if (i + (dual ? 2 : 1) >= tiles) next_queries(i + 1 == tiles);
           if (any_row) {
-            const bool edge = k0 + kKT > (pre ? a.prefix_len : all_see);
-            const int seen = pre ? a.prefix_len : lim;
             uint32_t p[64];
             float2 lt, lrt;
             // The weights are taken against the reference maximum as it stands;
@@ -543,16 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // reference moved to the maximum and the tile, still in tensor
             // memory, done again: once, after which no weight passes 2^bias.
             // The first tile sets it beforehand.
-            uint32_t vis[4];  // TREE: the tile's keys that the row sees
-            bool sees = k0 < seen;
-            if (TREE && edge) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                vis[c] = low_bits(seen - k0 - c * 32);
-                if (bits && !pre) vis[c] &= tree_window(bits, a.tree_words, k0 + c * 32 - all_see);
-              }
-              sees = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
-            }
             auto mask = [&](uint32_t(&v)[32], int c) {
               if (TREE) {
                 if (edge) {
@@ -567,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (k0 + c * 32 + e >= seen) v[e] = 0xff800000u;
               }
             };
-            bool move = i == 0;
+            bool move = first;
 #pragma unroll 1
             while (true) {  // a pass that moves the reference is the last
               if (move) {
@@ -590,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l2.y *= f;
                 lr2.x *= f;
                 lr2.y *= f;
-                if (i > 0) {
-                  if (kAhead) {  // the P V before has been issued, but need not be over
+                if (!first) {
+                  if (kAhead && !dual) {  // the P V before has been issued, but need not be over
                     const int j = i - 1;
                     mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
                     __syncwarp();
@@ -646,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN)
             // the tile's values' place in the ring
-            int z = 2 * i + (kAhead && i + 1 < tiles ? 2 : 1) + vst;
+            int z = 2 * i + ((kAhead || dual) && i + 1 < tiles ? 2 : 1) + vst;
             const uint32_t zph = vph ^ ((uint32_t)(z / stages) & 1u);
             z %= stages;
             const bool there = mbar_wait(&full[z], zph, abort_flag, a.err);
@@ -673,12 +723,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         vph ^= (uint32_t)(z / stages) & 1u;
         vst = z % stages;
       }
-      if (!used) {
-        more = peek_segment();
-        more_used = more && uses(&segs[slot_i]);
-        if (more_used) load_q(&segs[slot_i]);
-      }
-      if (used) {
+      if (!used) next_queries(false);
+      if (dual && t == 1) {
+        // (the other stream's warps take the queries that came in here for theirs)
+        cp_async_wait_all();
+        fence_async_smem();
+        ml[r_lane] = make_float4(mref, l2.x + l2.y, RSUM ? lr2.x + lr2.y : 0.f, 0.f);
+        arrive(ml_full);
+      } else if (dual) {
+        bool got = mbar_wait(ml_full, dph, abort_flag, a.err);
+        got = got && mbar_wait(d_full, dph, abort_flag, a.err);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any_row) {
+          const bool done = whole(ln, *cur);
+          const int2 at = cur->parts ? row_place(a, *cur, r) : make_int2(0, 0);
+          const float4 y = ml[r_lane];
+          const float m = fmaxf(mref, y.x);
+          const float f0 = mref == m ? 1.f : exp2_fast((mref - m) * sc), f1 = y.x == m ? 1.f : exp2_fast((y.x - m) * sc);
+          const float l = (l2.x + l2.y) * f0 + y.y * f1, lr = RSUM ? (lr2.x + lr2.y) * f0 + y.z * f1 : l;
+          const float w = done ? inverse_sum(lr) : l == lr ? 1.f : l / lr;
+          const float w0 = f0 * w, w1 = f1 * w;
+          float* dst = ln.part_o + (long long)(cur->prow + r) * DP;
+          T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D;
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32], o1[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld32(to + DP + c * 32, o1);
+            tmem_ld_wait_for(o);
+            tmem_ld_wait_for(o1);
+            if (r < cur->rows) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e]) * w0));
+              if (!done) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st_global_32(dst + c * 32 + e * 8, o + e * 8);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 v;
+                  v.x = Half16<T>::pack(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1]));
+                  v.y = Half16<T>::pack(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3]));
+                  v.z = Half16<T>::pack(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5]));
+                  v.w = Half16<T>::pack(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7]));
+                  if (c * 32 + e * 8 < a.D) *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = v;
+                }
+              }
+            }
+          }
+          if (r < cur->rows) {
+            if (!done)
+              ln.part_ml[cur->prow + r] = make_float2(m, l);
+            else if (a.lse)
+              a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(m, l, a.scale);
+            if (cur->parts) write_info(a, ln, *cur, r, at);
+          }
+        }
+        tc_fence_before();
+      } else if (used) {
         const int j = kAhead ? tiles - 1 : 0;
         const bool got = mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
         outs[0] += (uint32_t)(j >> 1) + 1u;  // tiles 0, 2, ... and 1, 3, ...
@@ -731,7 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
-      if (more_used) q_arrive();
+      if (dual) dph ^= 1u;
+      if (more_q) q_arrive();
       arrive(&seg_empty[cur - segs]);
       some = more;
       cur = &segs[slot_i];
@@ -764,8 +872,8 @@ template <typename T, int DP, bool RSUM, bool TREE>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
                    cudaStream_t s, bool pdl) {
   int stages = kMaxStages;  // as many as fit
-  while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
-  const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
+  while (stages > 2 && smem_plan(DP, stages, a.B, TREE).bytes + 1024 > 227 * 1024) --stages;
+  const size_t smem = smem_plan(DP, stages, a.B, TREE).bytes + 1024;
   const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE>, smem);
   if (e != cudaSuccess) return e;
   return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
