@@ -92,10 +92,12 @@ class Accepted:
     next_tokens and context_lens [num_seqs], all int32."""
 
     def __init__(self, *, num_seqs: int, max_path: int, device="cuda", stream=None):
-        buf = _output((num_seqs * (max_path + 3),), torch.int32, device, stream)
         self.num_seqs, self.max_path = num_seqs, max_path
-        path, self.counts, self.next_tokens, self.context_lens = buf.split([num_seqs * max_path] + [num_seqs] * 3)
-        self.path = path.view(num_seqs, max_path)
+        # (one buffer and four views of it take twice as long)
+        self.path = _output((num_seqs, max_path), torch.int32, device, stream)
+        self.counts = _output((num_seqs,), torch.int32, device, stream)
+        self.next_tokens = _output((num_seqs,), torch.int32, device, stream)
+        self.context_lens = _output((num_seqs,), torch.int32, device, stream)
 
 
 class PagedAttention:

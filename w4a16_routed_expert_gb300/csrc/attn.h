@@ -125,7 +125,11 @@ constexpr int rows_most(int D, bool tree) { return tree ? (D <= 64 ? 64 : 32) : 
 // 16000 prefix keys of 16 heads (0.1, 1.5, 6.1 million) 15 / 23, 24 / 31, 44 /
 // 48 us; 96 rows over 4000, 16000 of 8 heads (3.1, 12) 23 / 27, 54 / 38; 256
 // rows of 64 over 1000, 4000 (2.0, 8.2) 21 / 24, 33 / 27.
-constexpr long long kFewTriples = 1LL << 22;
+// Over trees, whose row groups read a key once for 32 rows and more: 128
+// tokens of up to 64 rows of 64 over 4000 keys (8.8 million) 37 / 33 us, over
+// 2000 of 128-wide heads (4.4) 36 / 41; 300 tokens of 128-wide heads over 1000
+// (9.6) 77 / 75.
+constexpr long long few_triples(bool tree) { return tree ? 1LL << 23 : 1LL << 22; }
 constexpr int kRowsKeyTile = 64;
 struct AttnRowsPlan {
   int n_cta, stages, row_groups;

@@ -79,6 +79,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   constexpr int WK = kWarps / WR;      // key groups
   constexpr int RB = WR * MT * 16;     // rows of a group at most
+  // Sixteens of keys that a warp takes in one step: more of them share a step's
+  // chain of waits (products, maximum, exponentials, products). (50
+  // trees of up to 52 rows of 64: 26.7 us, 29.6 with one sixteen a step; 64 rows
+  // of 128 over 8 sequences of 15000 keys 135 and 156.)
+  constexpr int KS = WR == 1 ? 1 : DP == 64 ? WR : 2;
   const SmemPlan sp = smem_plan(DP, MT, WR, ln.part_rows, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
@@ -289,71 +294,95 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 #pragma unroll 1
       for (int i = 0; i < s.tiles; ++i) {
+        // TREE: the bits of this warp's keys, asked for before the wait
+        constexpr int NV = (WR + 1) / 2;
+        uint32_t vis[MT][2][NV];
+        if (TREE) {
+          const int k0 = (s.tile + i) * kKT + wk * WR * 16;
+          if (k0 + WR * 16 > all_see) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int w = 0; w < NV; ++w) {
+                  vis[m][e][w] = low_bits(s.klen - k0 - w * 32);
+                  if (s.b >= 0)
+                    vis[m][e][w] &= tree_window(a.tree + lim[m][e], a.tree_words, k0 + w * 32 - all_see);
+                }
+          }
+        }
         const bool got = mbar_wait(&full[st], ph, abort_flag, a.err);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
 #pragma unroll 1
-        for (int sub = 0; sub < WR && (WR == 1 || wr * MT * 16 < s.rows); ++sub) {
-        const int key = (wk * WR + sub) * 16, k0 = (s.tile + i) * kKT + key;
-        const uint32_t kb = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes + keys_off(key);
-        const uint32_t vb = kb + kTileBytes;
-        const int here = s.nkeys - k0;  // keys of this warp's sixteen that exist
-        if (here > 0) {
-          if (here < 16) {
+        for (int sub = 0; sub < WR / KS && (WR == 1 || wr * MT * 16 < s.rows); ++sub) {
+          const int key = (wk * WR + sub * KS) * 16, k0 = (s.tile + i) * kKT + key;
+          const int here = s.nkeys - k0;  // keys of this step's that exist
+          if (here <= 0) break;
+          const uint32_t stage = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes;
+          uint32_t kb[KS];  // each sixteen keys (all in one box); the values kTileBytes behind them
+#pragma unroll
+          for (int j = 0; j < KS; ++j) kb[j] = stage + keys_off(key + 16 * j);
+          if (here < 16 * KS) {
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN); their logits are masked
-            for (int z = lane; z < (16 - here) * (DP / 8); z += 32) {
+            for (int z = lane; z < (16 * KS - here) * (DP / 8); z += 32) {
               const int r = here + z / (DP / 8), c8 = z % (DP / 8);
-              *reinterpret_cast<uint4*>(smem + (vb - smem_u32(smem)) + (uint32_t)(c8 >> 3) * half_step +
-                                        (uint32_t)r * 128 + (uint32_t)((c8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(smem + (stage + kTileBytes - smem_u32(smem)) + keys_off(key + r) +
+                                        (uint32_t)(c8 >> 3) * half_step + (uint32_t)((c8 & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
           }
-          float sv[MT][2][4];
+          float sv[MT][2 * KS][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
               for (int e = 0; e < 4; ++e) sv[m][n][e] = 0.f;
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
-            uint32_t kf[4];
             const int c16 = (kk & 3) * 2;
-            ldsm4(kb + (uint32_t)(kk >> 2) * half_step + (uint32_t)krow * 128 +
-                      (uint32_t)(((c16 + ksel) ^ (krow & 7)) << 4),
-                  kf);
+            uint32_t qf[MT][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              uint32_t qf[4];
+            for (int m = 0; m < MT; ++m)
               ldsm4(qs + (uint32_t)(kk >> 2) * RB * 128 + (uint32_t)((wr * MT + m) * 16 + qrow) * 128 +
                         (uint32_t)(((c16 + qsel) ^ (qrow & 7)) << 4),
-                    qf);
-              mma16816<T>(sv[m][0], qf, kf[0], kf[1]);
-              mma16816<T>(sv[m][1], qf, kf[2], kf[3]);
-            }
-          }
-          uint32_t pf[MT][4], pl[MT][4];
+                    qf[m]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (TREE && k0 + 16 > all_see) {
+            for (int j = 0; j < KS; ++j) {
+              uint32_t kf[4];
+              ldsm4(kb[j] + (uint32_t)(kk >> 2) * half_step + (uint32_t)krow * 128 +
+                        (uint32_t)(((c16 + ksel) ^ (krow & 7)) << 4),
+                    kf);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t vis = low_bits(s.klen - k0);
-                if (s.b >= 0) vis &= tree_window(a.tree + lim[m][e], a.tree_words, k0 - all_see);
-                vis >>= t4 * 2;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  if (!((vis >> (n * 8)) & 1u)) sv[m][n][2 * e] = -INFINITY;
-                  if (!((vis >> (n * 8)) & 2u)) sv[m][n][2 * e + 1] = -INFINITY;
-                }
+              for (int m = 0; m < MT; ++m) {
+                mma16816<T>(sv[m][2 * j], qf[m], kf[0], kf[1]);
+                mma16816<T>(sv[m][2 * j + 1], qf[m], kf[2], kf[3]);
               }
             }
-            if (!TREE && k0 + 16 > all_see) {
+          }
+          uint32_t pf[MT][KS][4], pl[MT][KS][4];
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+          for (int m = 0; m < MT; ++m) {
+            if (TREE && k0 + 16 * KS > all_see) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int n = 0; n < 2 * KS; ++n) {
+                  const uint32_t word = WR > KS ? (sub ? vis[m][e][NV - 1] : vis[m][e][0]) : vis[m][e][n / 4];
+                  const uint32_t bits = word >> ((n & 3) * 8 + t4 * 2);
+                  if (!(bits & 1u)) sv[m][n][2 * e] = -INFINITY;
+                  if (!(bits & 2u)) sv[m][n][2 * e + 1] = -INFINITY;
+                }
+            }
+            if (!TREE && k0 + 16 * KS > all_see) {
+#pragma unroll
+              for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   if (k0 + n * 8 + t4 * 2 + (e & 1) >= lim[m][e >> 1]) sv[m][n][e] = -INFINITY;
@@ -362,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               mx[e] = fmaxf(fmaxf(sv[m][0][2 * e], sv[m][0][2 * e + 1]), fmaxf(sv[m][1][2 * e], sv[m][1][2 * e + 1]));
+#pragma unroll
+              for (int n = 2; n < 2 * KS; ++n) mx[e] = fmaxf(mx[e], fmaxf(sv[m][n][2 * e], sv[m][n][2 * e + 1]));
               mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
               mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
             }
@@ -379,48 +410,54 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
               }
             }
-            float p[2][4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float ref = mref[m][e] == -INFINITY ? 0.f : mref[m][e];
+            for (int j = 0; j < KS; ++j) {
+              float p[2][4];
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                float2 w = fadd2(make_float2(sv[m][n][2 * e], sv[m][n][2 * e + 1]), make_float2(-ref, -ref));
-                w = ffma2(w, make_float2(sc, sc), make_float2(ProbBias<T>::value, ProbBias<T>::value));
-                p[n][2 * e] = exp2_fast(w.x);
-                p[n][2 * e + 1] = exp2_fast(w.y);
-                l[m][e] += p[n][2 * e];
-                l[m][e] += p[n][2 * e + 1];
+              for (int e = 0; e < 2; ++e) {
+                const float ref = mref[m][e] == -INFINITY ? 0.f : mref[m][e];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  const float(&v)[4] = sv[m][2 * j + n];
+                  float2 w = fadd2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(-ref, -ref));
+                  w = ffma2(w, make_float2(sc, sc), make_float2(ProbBias<T>::value, ProbBias<T>::value));
+                  p[n][2 * e] = exp2_fast(w.x);
+                  p[n][2 * e + 1] = exp2_fast(w.y);
+                  l[m][e] += p[n][2 * e];
+                  l[m][e] += p[n][2 * e + 1];
+                }
               }
-            }
-            // the weights as two 16-bit numbers, the rounded one and what it
-            // leaves: with few rows their rounding would not average out, and
-            // the second product hides under the copies
+              // the weights as two 16-bit numbers, the rounded one and what it
+              // leaves: with few rows their rounding would not average out, and
+              // the second product hides under the copies
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float w0 = p[f >> 1][2 * (f & 1)], w1 = p[f >> 1][2 * (f & 1) + 1];
-              pf[m][f] = Half16<T>::pack(w0, w1);
-              const float2 r = Half16<T>::unpack(pf[m][f]);
-              pl[m][f] = Half16<T>::pack(w0 - r.x, w1 - r.y);
+              for (int f = 0; f < 4; ++f) {
+                const float w0 = p[f >> 1][2 * (f & 1)], w1 = p[f >> 1][2 * (f & 1) + 1];
+                pf[m][j][f] = Half16<T>::pack(w0, w1);
+                const float2 r = Half16<T>::unpack(pf[m][j][f]);
+                pl[m][j][f] = Half16<T>::pack(w0 - r.x, w1 - r.y);
+              }
             }
           }
 #pragma unroll
           for (int nn = 0; nn < DP / 16; ++nn) {
-            uint32_t vf[4];
             const int c16 = (nn & 3) * 2;
-            ldsm4t(vb + (uint32_t)(nn >> 2) * half_step + (uint32_t)vrow * 128 +
-                       (uint32_t)(((c16 + vsel) ^ (vrow & 7)) << 4),
-                   vf);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma16816<T>(o[m][2 * nn], pf[m], vf[0], vf[1]);
-              mma16816<T>(o[m][2 * nn + 1], pf[m], vf[2], vf[3]);
-              mma16816<T>(o[m][2 * nn], pl[m], vf[0], vf[1]);
-              mma16816<T>(o[m][2 * nn + 1], pl[m], vf[2], vf[3]);
+            for (int j = 0; j < KS; ++j) {
+              uint32_t vf[4];
+              ldsm4t(kb[j] + kTileBytes + (uint32_t)(nn >> 2) * half_step + (uint32_t)vrow * 128 +
+                         (uint32_t)(((c16 + vsel) ^ (vrow & 7)) << 4),
+                     vf);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816<T>(o[m][2 * nn], pf[m][j], vf[0], vf[1]);
+                mma16816<T>(o[m][2 * nn + 1], pf[m][j], vf[2], vf[3]);
+                mma16816<T>(o[m][2 * nn], pl[m][j], vf[0], vf[1]);
+                mma16816<T>(o[m][2 * nn + 1], pl[m][j], vf[2], vf[3]);
+              }
             }
           }
-          if (here < 16) fence_async_smem();  // the zeros before the stage's next copies
-        }
+          if (here < 16 * KS) fence_async_smem();  // the zeros before the stage's next copies
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
