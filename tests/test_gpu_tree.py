@@ -179,6 +179,10 @@ TREE = {  # dtype, Hq, Hk, D, page, order, nodes, context, prefix, what a token 
     "heads of 8": (F16, 3, 1, 8, 16, "slot", [5, 40], [9, 100], 70, "bushy"),
     "a long context": (BF16, 64, 8, 128, 64, "slot", [24, 48], [5000, 801], 0, "bushy"),
     "blocks of their own behind a prefix": (F16, 8, 1, 64, 16, "slot", [60, 40], [33, 0], 333, "bushy"),
+    "trees of one row block and of two": (BF16, 16, 2, 128, 64, "slot", [64, 20, 40, 1, 33], [3000, 500, 0, 90, 128], 0, "bushy"),
+    "the same behind a prefix of their own": (F16, 16, 2, 64, 32, "head", [64, 1, 2, 3, 5, 1, 1, 40], [700, 9, 0, 4000, 90, 130, 1, 64], 500, "chain"),
+    "the same read with the prefix": (F16, 24, 2, 128, 16, "slot", [60, 22, 43], [100, 0, 1500], 140, "bushy"),
+    "trees of three and four row blocks": (BF16, 8, 1, 96, 48, "head", [128, 97, 80], [0, 1000, 333], 0, "bushy"),
     "a tree wider than a tile": (F16, 4, 2, 64, 16, "slot", [300], [60], 0, "random"),
     "a tree of a thousand": (BF16, 2, 1, 64, 128, "slot", [1000], [130], 0, "bushy"),
     "many": (F16, 4, 4, 64, 16, "slot", [(3 * i) % 8 for i in range(130)], [(37 * i) % 150 for i in range(130)], 200, "bushy"),
