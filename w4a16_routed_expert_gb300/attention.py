@@ -95,9 +95,8 @@ class Accepted:
         self.num_seqs, self.max_path = num_seqs, max_path
         # (one buffer and four views of it take twice as long)
         self.path = _output((num_seqs, max_path), torch.int32, device, stream)
-        self.counts = _output((num_seqs,), torch.int32, device, stream)
-        self.next_tokens = _output((num_seqs,), torch.int32, device, stream)
-        self.context_lens = _output((num_seqs,), torch.int32, device, stream)
+        self.counts, self.next_tokens, self.context_lens = (_output((num_seqs,), torch.int32, device, stream)
+                                                            for _ in range(3))
 
 
 class PagedAttention:
@@ -261,10 +260,11 @@ class PagedAttention:
             out, op, os_ = self._new_rows(q, T, self.num_q_heads, stream)
         else:
             op, os_ = self._rows("out", out, T, self.num_q_heads)
-        if lse is None and return_lse:
-            lse = _output((T, self.num_q_heads), torch.float32, q.device, stream)
-        if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous()
-                                or lse.shape != (T, self.num_q_heads)):
+        if lse is None:
+            if return_lse:
+                lse = _output((T, self.num_q_heads), torch.float32, q.device, stream)
+        elif (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous()
+              or lse.shape != (T, self.num_q_heads)):
             raise ValueError(f"lse: contiguous cuda float32 [{T}][{self.num_q_heads}]")
         bt, ts = None, 0
         if block_table is not None and block_table.numel():

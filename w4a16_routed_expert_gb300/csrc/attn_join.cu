@@ -113,9 +113,91 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const JoinArgs j) {
   if (a.lse && lane == 0) a.lse[row] = log_sum<T>(m, l, a.scale);
 }
 
+// Over trees rows are many and their partials few: DP / 8 lanes a row, 2 (4 at
+// DP 64) rows a warp, a row's partials one after the other with kAhead of them
+// asked for together; no lane waits for another. FIGURES_JOIN
+template <typename T, int DP>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join_rows(const JoinArgs j) {
+  constexpr int W = DP / 8, kAhead = 4;
+  pdl_trigger();
+  pdl_wait();
+  const AttnArgs& a = j.a;
+  const int gl = threadIdx.x & (W - 1);
+  const long long row = (long long)blockIdx.x * (kJoinThreads / W) + threadIdx.x / W;
+  const bool mine = row < (long long)a.T * a.Hq;
+  int2 ip = make_int2(0, 0), io = make_int2(0, 0);
+  if (mine && j.prefix_step) ip = j.info_prefix[row];
+  if (mine && j.own_step) io = j.info_own[row];
+  __syncwarp();
+  if (mine && gl == 0) {
+    if (j.prefix_step) j.info_prefix[row] = make_int2(0, 0);
+    if (j.own_step) j.info_own[row] = make_int2(0, 0);
+  }
+  if (!mine || ip.y < 0 || io.y < 0) return;  // stored by the one block that had all its keys
+  const int n = ip.y + io.y;
+  const bool act = gl * 8 < a.D;
+  float m = -INFINITY, l = 0.f;
+  float o[8] = {};
+  const float sc = a.scale * kLog2e;
+  auto scale_to = [&](float mn, float mi) { return mi == mn ? 1.f : exp2_fast((mi - mn) * sc); };
+#pragma unroll 1
+  for (int i = 0; i < n; i += kAhead) {
+    float2 v[kAhead];
+    float4 p[kAhead], q[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = i + u;
+      p[u] = q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = make_float2(-INFINITY, 0.f);
+      if (k < n) {
+        const long long at = k < ip.y ? (long long)ip.x + (long long)k * j.prefix_step
+                                      : (long long)io.x + (long long)(k - ip.y) * j.own_step;
+        v[u] = j.part_ml[at];
+        if (act) {
+          p[u] = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8);
+          q[u] = *reinterpret_cast<const float4*>(j.part_o + at * DP + gl * 8 + 4);
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) mn = fmaxf(mn, v[u].x);
+    const float f = scale_to(mn, m);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float w = scale_to(mn, v[u].x);
+      l = fmaf(w, v[u].y, l);
+      const float x[8] = {p[u].x, p[u].y, p[u].z, p[u].w, q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(w, x[e], o[e]);
+    }
+  }
+  const float inv = inverse_sum(l);  // a row that sees no key: zeros
+  const int t = (int)(row / a.Hq), hq = (int)(row - (long long)t * a.Hq);
+  if (act) {
+    uint4 r;
+    r.x = Half16<T>::pack(o[0] * inv, o[1] * inv);
+    r.y = Half16<T>::pack(o[2] * inv, o[3] * inv);
+    r.z = Half16<T>::pack(o[4] * inv, o[5] * inv);
+    r.w = Half16<T>::pack(o[6] * inv, o[7] * inv);
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)t * a.out_stride + (long long)hq * a.D + gl * 8) = r;
+  }
+  if (a.lse && gl == 0) a.lse[row] = log_sum<T>(m, l, a.scale);
+}
+
 template <typename T>
 cudaError_t launch(const JoinArgs& j, cudaStream_t s, bool pdl) {
   const long long rows = (long long)j.a.T * j.a.Hq;
+  if (j.a.tree) {
+    const int per = kJoinThreads / (j.DP / 8);
+    const dim3 blocks((unsigned)((rows + per - 1) / per));
+    return j.DP == 128 ? launch_ex(k_attn_join_rows<T, 128>, blocks, dim3(kJoinThreads), 0, s, pdl, j)
+                       : launch_ex(k_attn_join_rows<T, 64>, blocks, dim3(kJoinThreads), 0, s, pdl, j);
+  }
   const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   return j.DP == 128 ? launch_ex(k_attn_join<T, 128>, grid, dim3(kJoinThreads), 0, s, pdl, j)
                      : launch_ex(k_attn_join<T, 64>, grid, dim3(kJoinThreads), 0, s, pdl, j);
