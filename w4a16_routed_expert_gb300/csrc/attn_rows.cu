@@ -42,7 +42,7 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int MT, int WR, int rows, 
   p.q = (uint32_t)stages * 2 * kKT * DP * 2;
   p.merge = p.q + (uint32_t)WR * MT * 16 * DP * 2;
   p.ml = p.merge + (WR == 4 ? 0u : 2u * MT * (rows > 8 ? 16 : 8) * DP * 4);
-  p.bars = p.ml + (uint32_t)kWarps * MT * 16 * 8;
+  p.bars = p.ml + (uint32_t)kWarps * MT * 16 * (WR > 1 ? 16 : 8);
   p.seg = p.bars + 2 * (kMaxStages + kSegSlots) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 64;
@@ -84,6 +84,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   // trees of up to 52 rows of 64: 26.7 us, 29.6 with one sixteen a step; 64 rows
   // of 128 over 8 sequences of 15000 keys 135 and 156.)
   constexpr int KS = WR == 1 ? 1 : DP == 64 ? WR : 2;
+  // The weights as two 16-bit numbers, the rounded one and what it leaves: with
+  // few rows their rounding would not average out, and the second product hides
+  // under the copies. With several row groups it does not (16 trees of up to 31
+  // rows of 128 behind 1000 keys 53 us, 48 with one): there one, and the quotient
+  // by the sum of the rounded weights (as in the tcgen05 kernel).
+  constexpr bool kTwoParts = WR == 1;
   const SmemPlan sp = smem_plan(DP, MT, WR, ln.part_rows, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
@@ -212,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t qs = smem_u32(smem + sp.q);
     const int qrow = (lane & 7) + (((lane >> 3) & 1) << 3), qsel = lane >> 4;
     float2* ml = reinterpret_cast<float2*>(smem + sp.ml);
+    float* mlr = reinterpret_cast<float*>(ml + kWarps * MT * 16);
     float* merge = reinterpret_cast<float*>(smem + sp.merge);
     int st = 0, slot_i = 0;
     uint32_t ph = 0, sph = 0;
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (bar_any(!ok) || !some) break;
       float o[MT][DP / 8][4];
-      float mref[MT][2], l[MT][2];
+      float mref[MT][2], l[MT][2], lr[MT][2];  // reference, sum of the weights, of the rounded ones
       int lim[MT][2];  // keys each of the lane's rows sees; TREE: where its token's bits are
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mref[m][e] = -INFINITY;
-          l[m][e] = 0.f;
+          l[m][e] = lr[m][e] = 0.f;
           const int row = s.row0 + min((wr * MT + m) * 16 + g8 + 8 * e, s.rows - 1);
           if (TREE)
             lim[m][e] = (s.t0 + row / a.g) * a.tree_words;
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
           }
-          uint32_t pf[MT][KS][4], pl[MT][KS][4];
+          uint32_t pf[MT][KS][4], pl[kTwoParts ? MT : 1][KS][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (TREE && k0 + 16 * KS > all_see) {
@@ -403,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const float f = mref[m][e] == mn ? 1.f : exp2_fast((mref[m][e] - mn) * sc);
                 mref[m][e] = mn;
                 l[m][e] *= f;
+                if (!kTwoParts) lr[m][e] *= f;
 #pragma unroll
                 for (int n = 0; n < DP / 8; ++n) {
                   o[m][n][2 * e] *= f;
@@ -427,15 +435,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                   l[m][e] += p[n][2 * e + 1];
                 }
               }
-              // the weights as two 16-bit numbers, the rounded one and what it
-              // leaves: with few rows their rounding would not average out, and
-              // the second product hides under the copies
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 const float w0 = p[f >> 1][2 * (f & 1)], w1 = p[f >> 1][2 * (f & 1) + 1];
                 pf[m][j][f] = Half16<T>::pack(w0, w1);
                 const float2 r = Half16<T>::unpack(pf[m][j][f]);
-                pl[m][j][f] = Half16<T>::pack(w0 - r.x, w1 - r.y);
+                if (kTwoParts)
+                  pl[kTwoParts ? m : 0][j][f] = Half16<T>::pack(w0 - r.x, w1 - r.y);
+                else
+                  lr[m][f & 1] += r.x + r.y;  // (row g8 + 8 (f & 1))
               }
             }
           }
@@ -452,8 +460,10 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int m = 0; m < MT; ++m) {
                 mma16816<T>(o[m][2 * nn], pf[m][j], vf[0], vf[1]);
                 mma16816<T>(o[m][2 * nn + 1], pf[m][j], vf[2], vf[3]);
-                mma16816<T>(o[m][2 * nn], pl[m][j], vf[0], vf[1]);
-                mma16816<T>(o[m][2 * nn + 1], pl[m][j], vf[2], vf[3]);
+                if (kTwoParts) {
+                  mma16816<T>(o[m][2 * nn], pl[m][j], vf[0], vf[1]);
+                  mma16816<T>(o[m][2 * nn + 1], pl[m][j], vf[2], vf[3]);
+                }
               }
             }
           }
@@ -482,25 +492,33 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 1);
           l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], 2);
           if (t4 == 0) ml[r0 + m * 16 + g8 + 8 * e] = make_float2(mref[m][e], l[m][e]);
+          if (!kTwoParts) {
+            lr[m][e] += __shfl_xor_sync(0xffffffffu, lr[m][e], 1);
+            lr[m][e] += __shfl_xor_sync(0xffffffffu, lr[m][e], 2);
+            if (t4 == 0) mlr[r0 + m * 16 + g8 + 8 * e] = lr[m][e];
+          }
         }
       bar_compute();
       if (kAsyncQ && some) load_q(s);
-      float mt[MT][2], lt[MT][2];
+      float mt[MT][2], lt[MT][2], lrt[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = (wr * MT + m) * 16 + g8 + 8 * e;
-          float mm = -INFINITY, ll = 0.f;
+          float mm = -INFINITY, ll = 0.f, lq = 0.f;
 #pragma unroll
           for (int w = 0; w < WK; ++w) mm = fmaxf(mm, ml[w * RB + r].x);
 #pragma unroll
           for (int w = 0; w < WK; ++w) {
             const float2 v = ml[w * RB + r];
-            ll += v.y * (v.x == mm ? 1.f : exp2_fast((v.x - mm) * sc));
+            const float x = v.x == mm ? 1.f : exp2_fast((v.x - mm) * sc);
+            ll += v.y * x;
+            if (!kTwoParts) lq += mlr[w * RB + r] * x;
           }
           mt[m][e] = mm;
           lt[m][e] = ll;
+          lrt[m][e] = kTwoParts ? ll : lq;
           const float f = mref[m][e] == mm ? 1.f : exp2_fast((mref[m][e] - mm) * sc);
 #pragma unroll
           for (int n = 0; n < DP / 8; ++n) {
@@ -546,7 +564,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (r < cur.rows) {
               const bool done = whole(ln, cur);
               const int2 at = cur.parts ? row_place(a, cur, r) : make_int2(0, 0);
-              const float inv = inverse_sum(lt[m][e]);
+              const float inv = inverse_sum(lrt[m][e]);
+              // a partial stands against the exact sum
+              const float own = kTwoParts || lt[m][e] == lrt[m][e] ? 1.f : lt[m][e] / lrt[m][e];
               float* dst = ln.part_o + (long long)(cur.prow + r) * DP + t4 * 2;
               T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D + t4 * 2;
 #pragma unroll
@@ -554,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const float2 v = WK > 1 ? src[((e * MT + m) * (DP / 8) + n) * 32] : make_float2(0.f, 0.f);
                 const float2 w = make_float2(o[m][n][2 * e] + v.x, o[m][n][2 * e + 1] + v.y);
                 if (!done)
-                  *reinterpret_cast<float2*>(dst + n * 8) = w;
+                  *reinterpret_cast<float2*>(dst + n * 8) = kTwoParts ? w : make_float2(w.x * own, w.y * own);
                 else if (n * 8 < a.D)
                   *reinterpret_cast<uint32_t*>(out + n * 8) = Half16<T>::pack(w.x * inv, w.y * inv);
               }
