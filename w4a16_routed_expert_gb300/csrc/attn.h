@@ -113,12 +113,16 @@ bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int 
 // beside a second block (20 rows of 128 over 16 sequences of 8000 keys: 173 us,
 // 138 with one block an SM, 95 on the tcgen05 tiles; at 64, 20 rows behind 8192
 // keys: 23 us, 29 on the tcgen05 tiles).
-// Over trees up to 64 and 32, the warps as 1 by 4, 2 by 2 or 4 by 1 groups of 16
-// rows and of keys (50 trees of up to 52 rows of 64 with up to 713 keys: 30 us,
-// 42 on the tcgen05 tiles; 16 of up to 31 rows of 128 with up to 2600 keys: 44
-// and 51; but 64 rows of 128 over 8 sequences of 15000 keys: 156 and 85).
+// Over trees up to 64, the warps as 1 by 4, 2 by 2 or 4 by 1 groups of 16 rows
+// and of keys, at head sizes above 64 up to 32 where contexts may be long: 16
+// trees of 64 rows of 128 to a key after 100, 500, 2000 keys 18, 32, 62 us (24,
+// 35, 59 on the tcgen05 tiles), 64 trees after 100 keys 52 (70), but 8 after
+// 15000 keys 107 (86): there the products bind. 128 rows after 500 keys 57 (39).
 constexpr int kRowsMax = 64;
-constexpr int rows_most(int D, bool tree) { return tree ? (D <= 64 ? 64 : 32) : D <= 64 ? 32 : 16; }
+constexpr int kRowsLong = 4096;  // own keys
+constexpr int rows_most(int D, bool tree, int max_keys) {
+  return tree ? (D <= 64 || max_keys <= kRowsLong ? 64 : 32) : D <= 64 ? 32 : 16;
+}
 // (query token, query head, prefix key) triples up to which it takes the
 // prefix's rows beside few own rows, however many. In its launch / in one of
 // the tcgen05 kernel before it, own keys to 200: 24 rows of 128 over 300, 4000,

@@ -197,7 +197,7 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
   // stays in the few-row kernel's launch while there is little to compute, in
   // row blocks that read its keys once each.
   const bool over_tree = a.tree != nullptr;
-  const int most = moe::rows_most(a.D, over_tree);
+  const int most = moe::rows_most(a.D, over_tree, a.max_seq_len);
   const bool little = own_rows && (long long)a.T * a.Hq * a.prefix_len <= moe::few_triples(over_tree);
   const bool tile_own = own_rows > most;
   const bool tile_prefix = prefix_rows && (tile_own || (prefix_rows > most && !little));

@@ -607,7 +607,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
   if constexpr (TREE) {
     if (p.row_groups == 4) return run(k_attn_rows<T, DP, 1, 4, true>);
     if (p.row_groups == 2) return run(k_attn_rows<T, DP, 1, 2, true>);
-  } else if constexpr (rows_most(DP, false) > 16) {
+  } else if constexpr (rows_most(DP, false, 0) > 16) {
     if (ln.part_rows > 16) return run(k_attn_rows<T, DP, 2, 1, false>);
   }
   return run(k_attn_rows<T, DP, 1, 1, TREE>);
