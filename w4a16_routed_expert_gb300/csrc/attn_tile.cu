@@ -53,14 +53,13 @@ constexpr int kMaxStages = 8;
 constexpr float kSumMost = 32768.f;
 
 struct SmemPlan {
-  uint32_t ring, ml, bars, seg, misc, off, bytes;
+  uint32_t ring, bars, seg, misc, off, bytes;
 };
-__host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B, bool tree) {
+__host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
   SmemPlan p;
   p.ring = 2u * 128 * DP * 2;  // after the queries
-  p.ml = p.ring + (uint32_t)stages * kKT * DP * 2;
-  p.bars = p.ml + (tree ? 128u * 16u : 0u);
-  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 18) * 8;
+  p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
+  p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 19) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
   p.off = p.misc + 80;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
@@ -85,8 +84,8 @@ static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 // j in stream j mod 2 (`dual`): both S and O tiles hold the same rows, so that
 // one stream's products run under the other's softmax as they do for two row
 // tiles, and the streams' sums are joined where the part ends. Trees mostly have
-// such parts (8 sequences of 15000 keys, 64 key rows of 128: 85 us, 91 with one
-// stream; 32 rows: 84 and 106).
+// such parts (8 sequences of 15000 keys, 128 rows of 128 to a key: 88 us, 98 with
+// one stream; 1024 groups of 128 rows and up to 228 keys: 71).
 template <typename T, int DP, bool RSUM, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kOut = kAhead ? 384 : 256;     // columns of the output tiles
   constexpr uint32_t kHalf = 128 * 128;             // bytes of 64 elements of 128 rows
   constexpr uint32_t kTileBytes = NH * kHalf;       // a query, key or value tile
-  const SmemPlan sp = smem_plan(DP, stages, a.B, TREE);
+  const SmemPlan sp = smem_plan(DP, stages, a.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kMaxStages;
   uint64_t* q_full = empty + kMaxStages;  // [2] queries in shared memory and the output tile drained
@@ -117,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_empty = seg_full + kSegSlots;
   uint64_t* drain = seg_empty + kSegSlots;
   uint64_t* d_full = drain + 1;   // both streams' output complete
-  uint64_t* ml_full = d_full + 1; // the second stream's maxima and sums in shared memory
+  uint64_t* ml_full = d_full + 1; // both streams' references and sums in tensor memory
+  uint64_t* o_read = ml_full + 1; // the second stream's warps have read both outputs
   Segment* segs = reinterpret_cast<Segment*>(smem + sp.seg);
   Misc* misc = reinterpret_cast<Misc*>(smem + sp.misc);
   int32_t* own_off = reinterpret_cast<int32_t*>(smem + sp.off);
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     mbar_init(d_full, 1);
-    mbar_init(ml_full, 4);
+    mbar_init(ml_full, 8);
+    mbar_init(o_read, 4);
     misc->abort_flag = 0;
     misc->issued = 0;
     misc->mma_issued = 0;
@@ -519,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     auto uses = [&](const Segment* s) { return t == 0 || s->rows > 128 || is_dual(*s); };
-    float4* ml = reinterpret_cast<float4*>(smem + sp.ml);
-    uint32_t dph = 0;  // d_full, ml_full
+    uint32_t dph = 0;  // d_full, ml_full, o_read
     auto q_arrive = [&]() {
       cp_async_wait_all();
       fence_async_smem();
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (i + (dual ? 2 : 1) >= tiles) next_queries(i + 1 == tiles);
+          if (!TREE && i + 1 == tiles) next_queries(true);
           if (any_row) {
             uint32_t p[64];
             float2 lt, lrt;
@@ -715,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           arrive(&p_full[2 * t + par]);
+          // (over trees parts are many and short, and their first softmax should not wait)
+          if (TREE && !dual && i + 1 == tiles) next_queries(true);
         }
       }
       if (!ok) break;
@@ -724,13 +726,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         vst = z % stages;
       }
       if (!used) next_queries(false);
-      if (dual && t == 1) {
-        // (the other stream's warps take the queries that came in here for theirs)
-        cp_async_wait_all();
-        fence_async_smem();
-        ml[r_lane] = make_float4(mref, l2.x + l2.y, RSUM ? lr2.x + lr2.y : 0.f, 0.f);
+      if (dual) {
+        // The streams' references and sums change hands in the upper halves of
+        // their S columns (the weights stand in the lower ones); then the warps of
+        // each store half of the columns of the joined output.
+        const uint32_t mine = tmem + lanes + 64;
+        tmem_st4(mine + t * 128, make_float4(mref, l2.x + l2.y, RSUM ? lr2.x + lr2.y : 0.f, 0.f));
+        tmem_st_wait();
+        tc_fence_before();
         arrive(ml_full);
-      } else if (dual) {
+        next_queries(((tiles - 1) & 1) == t);
         bool got = mbar_wait(ml_full, dph, abort_flag, a.err);
         got = got && mbar_wait(d_full, dph, abort_flag, a.err);
         if (!__all_sync(0xffffffffu, got)) {
@@ -741,19 +746,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any_row) {
           const bool done = whole(ln, *cur);
           const int2 at = cur->parts ? row_place(a, *cur, r) : make_int2(0, 0);
-          const float4 y = ml[r_lane];
-          const float m = fmaxf(mref, y.x);
-          const float f0 = mref == m ? 1.f : exp2_fast((mref - m) * sc), f1 = y.x == m ? 1.f : exp2_fast((y.x - m) * sc);
-          const float l = (l2.x + l2.y) * f0 + y.y * f1, lr = RSUM ? (lr2.x + lr2.y) * f0 + y.z * f1 : l;
+          const float4 x = tmem_ld4(mine), y = tmem_ld4(mine + 128);
+          const float m = fmaxf(x.x, y.x);
+          const float f0 = x.x == m ? 1.f : exp2_fast((x.x - m) * sc), f1 = y.x == m ? 1.f : exp2_fast((y.x - m) * sc);
+          const float l = x.y * f0 + y.y * f1, lr = RSUM ? x.z * f0 + y.z * f1 : l;
           const float w = done ? inverse_sum(lr) : l == lr ? 1.f : l / lr;
           const float w0 = f0 * w, w1 = f1 * w;
           float* dst = ln.part_o + (long long)(cur->prow + r) * DP;
           T* out = static_cast<T*>(a.out) + (long long)at.x * a.out_stride + (long long)at.y * a.D;
 #pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
+          for (int c = t * (DP / 64); c < (t + 1) * (DP / 64); ++c) {
             uint32_t o[32], o1[32];
-            tmem_ld32(to + c * 32, o);
-            tmem_ld32(to + DP + c * 32, o1);
+            tmem_ld32(tmem + lanes + kOut + c * 32, o);
+            tmem_ld32(tmem + lanes + kOut + DP + c * 32, o1);
             tmem_ld_wait_for(o);
             tmem_ld_wait_for(o1);
             if (r < cur->rows) {
@@ -776,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (r < cur->rows) {
+          if (t == 0 && r < cur->rows) {
             if (!done)
               ln.part_ml[cur->prow + r] = make_float2(m, l);
             else if (a.lse)
@@ -785,6 +790,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
+        if (t == 1) {
+          cp_async_wait_all();  // (queries that came in here may be the other warps' to hand on)
+          fence_async_smem();
+          arrive(o_read);
+        } else {
+          // (the next part's products may overwrite the outputs once its queries are handed on)
+          const bool read = mbar_wait(o_read, dph, abort_flag, a.err);
+          if (!__all_sync(0xffffffffu, read)) {
+            ok = false;
+            break;
+          }
+        }
       } else if (used) {
         const int j = kAhead ? tiles - 1 : 0;
         const bool got = mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
@@ -872,8 +889,8 @@ template <typename T, int DP, bool RSUM, bool TREE>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
                    cudaStream_t s, bool pdl) {
   int stages = kMaxStages;  // as many as fit
-  while (stages > 2 && smem_plan(DP, stages, a.B, TREE).bytes + 1024 > 227 * 1024) --stages;
-  const size_t smem = smem_plan(DP, stages, a.B, TREE).bytes + 1024;
+  while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
+  const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
   const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE>, smem);
   if (e != cudaSuccess) return e;
   return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
