@@ -180,7 +180,8 @@ moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride,
  * m of which are its m query tokens', token i sees the first n - m and key
  * n - m + j where bit j % 32 of tree[token * tree_stride + j / 32] is set; a
  * row with no bit sees not even itself. Bits from m on are ignored. The prefix
- * is seen by all; batch->causal is not looked at.
+ * is seen by all; batch->causal is not looked at. Tokens behind the last
+ * sequence's get zeros (as in moe_attn_forward), so that a step may be padded.
  *   tree         device [T][tree_stride]
  *   tree_stride  words of a token, at least max_q_len / 32 rounded up;
  *                T * tree_stride below 2^31
@@ -223,7 +224,7 @@ typedef struct {
  * -1 and no bits; ring places and table entries that the step does not give out
  * or take back stay as they were. One plan at a time per handle. A length,
  * parent, page or count out of range (a context that is negative, a sequence
- * longer than its row of the table, more tokens than T or max_nodes, a parent
+ * longer than its row of the table or 2^30, more tokens than T or max_nodes, a parent
  * not before its child, a free page beyond the cache) is recorded (moe_attn_sync:
  * MOE_ERR_INVALID_ARG); such a sequence is not served, such a token has slot -1
  * or no parent. */
@@ -257,7 +258,7 @@ moe_status_t moe_attn_accept(moe_attn_t* attn, const moe_attn_accept_t* accept, 
 /* Moves the keys and values of each sequence's accepted nodes: those of node
  * path[b][i] to key seq_lens[b] - m + i for i < counts[b], m the sequence's
  * tokens; in the caches of all n handles, which must be of one shape, type and
- * strides and no cache twice.
+ * strides and no cache twice (one handle's keys and values may be one cache).
  *   path    device [num_seqs][path_stride], ascending from i or more
  *   counts  device [num_seqs]
  * Errors are recorded in attns[0]: a path or count out of order or range, a

@@ -138,7 +138,7 @@ def test_plan_reports_what_is_out_of_range():
     a.sync()
     assert good.slots.tolist() == [3, 4, 36, 37, 38, 39, 40, -1]
     for bad, where in ((dict(context=(-1, 20)), 0), (dict(new=(-2, 5)), 0), (dict(held=(4, 2)), 0), (dict(held=(-1, 2)), 0),
-                       (dict(context=(3, 47)), 1), (dict(new=(2, 7)), 1), (dict(context=(3, 2 ** 31 - 1)), 1),
+                       (dict(context=(3, 47)), 1), (dict(new=(2, 7)), 1), (dict(context=(3, 2 ** 31 - 1)), 1), (dict(context=(3, 2 ** 30)), 1),
                        (dict(table=((12, -1, -1), (1, 2, -1))), 0), (dict(table=((0, 0, 0), (1, -1, -1))), 1),
                        (dict(context=(3, 40), ring=(3, 99, 5, 6, 7, 8, 9, 10), held=(1, 1)), 1), (dict(new=(2, 6), T=7), 1)):
         t = run(**bad)
@@ -183,6 +183,8 @@ TREE = {  # dtype, Hq, Hk, D, page, order, nodes, context, prefix, what a token 
     "the same behind a prefix of their own": (F16, 16, 2, 64, 32, "head", [64, 1, 2, 3, 5, 1, 1, 40], [700, 9, 0, 4000, 90, 130, 1, 64], 500, "chain"),
     "the same read with the prefix": (F16, 24, 2, 128, 16, "slot", [60, 22, 43], [100, 0, 1500], 140, "bushy"),
     "trees of three and four row blocks": (BF16, 8, 1, 96, 48, "head", [128, 97, 80], [0, 1000, 333], 0, "bushy"),
+    "two streams of many rows": (BF16, 64, 8, 128, 64, "slot", [12, 16, 10, 9, 15, 16], [5000, 300, 0, 127, 200, 131], 0, "bushy"),
+    "two streams of many rows of 64": (F16, 64, 4, 64, 16, "head", [7, 8, 5, 6, 8, 8, 8, 8, 8, 8], [300, 0, 127, 900, 131, 500, 64, 65, 1000, 2], 0, "chain"),
     "a tree wider than a tile": (F16, 4, 2, 64, 16, "slot", [300], [60], 0, "random"),
     "a tree of a thousand": (BF16, 2, 1, 64, 128, "slot", [1000], [130], 0, "bushy"),
     "many": (F16, 4, 4, 64, 16, "slot", [(3 * i) % 8 for i in range(130)], [(37 * i) % 150 for i in range(130)], 200, "bushy"),
@@ -378,6 +380,20 @@ def test_keep_moves_the_branch(name):
     attns[0].sync()
     for layer, w in zip(kv, want):
         assert torch.equal(layer[0], w[0]) and torch.equal(layer[1], w[1])
+
+
+def test_keep_of_keys_that_are_the_values():
+    """One tensor as both caches is moved once."""
+    c = torch.arange(4 * 16, device="cuda").half().view(4, 16, 1, 1).expand(4, 16, 2, 64).contiguous()
+    a = PagedAttention(num_q_heads=2, num_kv_heads=2, head_dim=64, k_cache=c, v_cache=c)
+    a.keep(ints([[0, 2, 3, 7]]), ints([4]), q_offsets=ints([0, 9]), seq_lens=ints([20]), max_seq_len=32, block_table=ints([[1, 3]]))
+    a.sync()
+    was = list(range(64))
+    want = list(was)
+    at = lambda j: (1, 3)[j // 16] * 16 + j % 16  # noqa: E731
+    for i, p in enumerate([0, 2, 3, 7]):
+        want[at(11 + i)] = was[at(11 + p)]
+    assert c[:, :, 1, 5].flatten().tolist() == want
 
 
 def test_keep_reports_what_is_out_of_range():

@@ -191,11 +191,12 @@ struct AcceptArgs {
 };
 cudaError_t launch_attn_accept(const AcceptArgs& a, cudaStream_t s, bool pdl);
 
-// Accepted nodes' keys and values of up to kKeepLayers caches to their places.
-constexpr int kKeepLayers = 32;
+// Accepted nodes' keys and values in up to kKeepCaches cache tensors to their
+// places.
+constexpr int kKeepCaches = 64;
 struct KeepArgs {
-  void* kv[2 * kKeepLayers];  // keys, values of each layer
-  int layers, B, Hk, D, page_size, num_pages, max_seq_len, table_stride, path_stride;
+  void* caches[kKeepCaches];
+  int count, B, Hk, D, page_size, num_pages, max_seq_len, table_stride, path_stride;
   long long page_stride, slot_stride, head_stride;
   const int32_t *q_offsets, *seq_lens, *block_table, *path, *counts;
   uint32_t* err;

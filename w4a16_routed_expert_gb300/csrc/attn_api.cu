@@ -648,6 +648,7 @@ moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs
   const char* fn = "moe_attn_keep";
   if (!attns || n < 1 || n > 1024) return set_error(MOE_ERR_INVALID_ARG, "%s: 1 to 1024 handles, got %d", fn, n);
   const void* caches[2 * 1024];
+  int count = 0;
   for (int32_t i = 0; i < n; ++i) {
     const moe_attn* h = attns[i];
     const moe_status_t st = check_handle(h, fn);
@@ -658,11 +659,11 @@ moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs
         c.page_size != f.page_size || c.num_pages != f.num_pages || c.page_stride != f.page_stride ||
         c.slot_stride != f.slot_stride || c.head_stride != f.head_stride)
       return set_error(MOE_ERR_INVALID_ARG, "%s: the cache of handle %d has another shape, type or strides", fn, i);
-    caches[2 * i] = h->buf.k_cache;
-    caches[2 * i + 1] = h->buf.v_cache;
+    caches[count++] = h->buf.k_cache;
+    if (h->buf.v_cache != h->buf.k_cache) caches[count++] = h->buf.v_cache;
   }
-  std::sort(caches, caches + 2 * n, std::less<const void*>());
-  if (std::adjacent_find(caches, caches + 2 * n) != caches + 2 * n)
+  std::sort(caches, caches + count, std::less<const void*>());
+  if (std::adjacent_find(caches, caches + count) != caches + count)
     return set_error(MOE_ERR_INVALID_ARG, "%s: the same cache twice", fn);
   const moe_attn* h = attns[0];
   if (num_seqs < 0 || num_seqs > 4096)
@@ -693,12 +694,9 @@ moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs
   a.path = path;
   a.counts = counts;
   a.err = h->err;
-  for (int32_t i = 0; i < n; i += moe::kKeepLayers) {
-    a.layers = std::min(n - i, moe::kKeepLayers);
-    for (int k = 0; k < a.layers; ++k) {
-      a.kv[2 * k] = attns[i + k]->buf.k_cache;
-      a.kv[2 * k + 1] = attns[i + k]->buf.v_cache;
-    }
+  for (int i = 0; i < count; i += moe::kKeepCaches) {
+    a.count = std::min(count - i, moe::kKeepCaches);
+    for (int k = 0; k < a.count; ++k) a.caches[k] = const_cast<void*>(caches[i + k]);
     const cudaError_t e = moe::launch_attn_keep(a, h->num_sms, static_cast<cudaStream_t>(stream), h->pdl);
     if (e != cudaSuccess) return cuda_error(e, fn);
   }

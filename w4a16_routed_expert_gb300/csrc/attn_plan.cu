@@ -55,7 +55,7 @@ __device__ __forceinline__ Ask ask_of(const PlanArgs& a, int ctx, int fresh, int
   Ask k;
   const long long keys = (long long)ctx + max(fresh, 0);
   k.valid = fresh >= -1 && held >= 0 && held <= a.table_stride &&
-            (fresh < 0 || (ctx >= 0 && keys <= (long long)a.table_stride * a.page_size)) &&
+            (fresh < 0 || (ctx >= 0 && keys <= min((long long)a.table_stride * a.page_size, 1LL << 30))) &&
             (a.max_nodes == 0 || fresh <= a.max_nodes);
   k.m = min(max(fresh, 0), a.T + 1);
   k.need = k.valid && fresh >= 0 ? max(0, (int)((keys + a.page_size - 1) / a.page_size) - held) : 0;
