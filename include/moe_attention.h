@@ -180,8 +180,9 @@ moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride,
  * m of which are its m query tokens', token i sees the first n - m and key
  * n - m + j where bit j % 32 of tree[token * tree_stride + j / 32] is set; a
  * row with no bit sees not even itself. Bits from m on are ignored. The prefix
- * is seen by all; batch->causal is not looked at. Tokens behind the last
- * sequence's get zeros (as in moe_attn_forward), so that a step may be padded.
+ * is seen by all; batch->causal is not looked at. A step may be padded: tokens
+ * behind the last sequence's change nothing in the others' rows; their own get
+ * zeros, or behind a prefix nothing of use.
  *   tree         device [T][tree_stride]
  *   tree_stride  words of a token, at least max_q_len / 32 rounded up;
  *                T * tree_stride below 2^31

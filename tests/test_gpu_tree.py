@@ -231,6 +231,33 @@ def test_forward_over_trees_matches_the_definition(name):
     assert torch.equal(a.forward(q.cuda(), tree=wide[:-1], **args), out)
 
 
+@pytest.mark.parametrize("prefix", [0, 30])
+@pytest.mark.parametrize("context", [20, 700])
+@pytest.mark.parametrize("node", [3, 90])
+def test_tokens_behind_the_last_sequence(node, context, prefix):
+    """A padded step: the other rows are those of the step without padding."""
+    nodes, own = [node, 2, 0], [context + node, 2, 40]
+    a, q, _, _, args = build(F16, 4, 2, 64, 16, "slot", nodes, own, prefix, seed=8)
+    bits = torch.cat([TO.pack(TO.branches(TO.random_tree(np.random.default_rng(1), m, "bushy")), 4) for m in nodes]).cuda()
+    want, wlse = a.forward(q.cuda(), tree=bits, return_lse=True, **args)
+    pad = 7
+    wide = PagedAttention(num_q_heads=4, num_kv_heads=2, head_dim=64, max_tokens=node + 2 + pad, max_seqs=4, k_cache=a._keep[0],
+                          v_cache=a._keep[1])
+    qp = torch.cat([q.cuda(), torch.full((pad, 4, 64), float("nan"), dtype=F16, device="cuda")])
+    bp = torch.cat([bits, torch.full((pad, 4), -1, dtype=torch.int32, device="cuda")])
+    args["max_q_len"] = node + pad
+    if prefix:  # (the number of tokens says how the prefix is read)
+        args["max_q_len"] = max(args["max_q_len"], (node + 2 + pad + 2) // 3)
+    out, lse = torch.full_like(qp, 9.0), torch.full((node + 2 + pad, 4), 9.0, device="cuda")
+    wide.forward(qp, tree=bp, out=out, lse=lse, **args)
+    wide.sync()
+    tol = 2.0 ** -9 * want.double().abs().cpu() + 2.0 ** -9  # (both round the weights and the result: 2^-11 each of values to 4)
+    within(out[:node + 2], want.double().cpu(), tol, "out")
+    assert ((lse[:node + 2] - wlse).abs() < 1e-4).all()
+    if not prefix:  # (a prefix is everybody's)
+        assert (out[node + 2:] == 0).all() and (lse[node + 2:] == -float("inf")).all()
+
+
 @pytest.mark.parametrize("name", ["few rows", "words end within tiles", "grouped heads behind a prefix", "heads of 96"])
 def test_a_line_is_a_tree(name):
     """Every token continues the one before: what causal attention gives."""

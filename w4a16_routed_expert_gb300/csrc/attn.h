@@ -82,6 +82,8 @@ struct LineArgs {
   float* part_o;         // [rows][DP]: block c's partial of a group stands at the group's first row + c * part_rows
   float2* part_ml;       // [rows] reference maximum (a logit before the scale), sum
   int2 *info_prefix, *info_own;  // [T][Hq] first partial row and number of partials, 0 between forwards
+  int whole;             // not 0: no line; a block takes whole groups of own keys, this many row blocks a sequence,
+                         // and stores their results: nothing is left to join
   int final_prefix, final_own;   // 1: these groups' rows have no other partials, one part alone is the result
 };
 // Rows of partial results one kernel can write.
@@ -135,6 +137,13 @@ constexpr int rows_most(int D, bool tree, int max_keys) {
 // (9.6) 77 / 75.
 constexpr long long few_triples(bool tree) { return tree ? 1LL << 23 : 1LL << 22; }
 constexpr int kRowsKeyTile = 64;
+// Over trees without a prefix, own keys up to which a block takes whole groups
+// (LineArgs::whole): the scan over the sequences, parts and the join's launch go,
+// for the time that a group's tiles take one block instead of several. 16 heads
+// of 128, trees of 16 tokens after up to 100, 250, 490 keys, whole / in a line:
+// one 7.6 / 8.5, 9.7 / 9.5, 12.0 / 10.4 us, 16 8.3 / 12.9, 10.6 / 15.4, 16.7 /
+// 19.6, 64 25.4 / 30.1, 32.4 / 35.8, 44.8 / 47.2; and the call's second launch.
+constexpr int kWholeKeys = 320;
 struct AttnRowsPlan {
   int n_cta, stages, row_groups;
   size_t smem;

@@ -254,6 +254,11 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
     fits = line(&few, block, moe::kRowsKeyTile, moe::kRowsWeight, plan.n_cta, few_prefix,
                 few_own) && fits;
   }
+  const bool whole = over_tree && few_own && !prefix_rows && a.max_seq_len <= moe::kWholeKeys;
+  if (whole) {
+    few.whole = (own_rows + few.row_block - 1) / few.row_block;
+    plan.n_cta = (int)std::min<long long>(plan.n_cta, (long long)a.B * a.Hk * few.whole);
+  }
   if (!fits) return set_error(MOE_ERR_INVALID_ARG, "%s: tokens and lengths beyond what one call takes", fn);
   // The join sets the words that it reads back to zero. Without it what the
   // kernels before it left is cleared behind them, on their own stream.
@@ -272,6 +277,7 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
                                                 tile.n_cta && h->pdl, s, h->pdl);
     if (e != cudaSuccess) return failed(e);
   }
+  if (whole) return MOE_OK;
   const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
   return e == cudaSuccess ? MOE_OK : failed(e);
 }
