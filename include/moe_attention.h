@@ -43,7 +43,7 @@
  * are rounded once when they are stored. (The probabilities that multiply
  * the values go to the tensor cores in the 16-bit type: in two parts, which
  * lose nothing beside the result's own rounding, where few rows read a key,
- * in one otherwise.)
+ * in one otherwise, and over trees from 17 rows on.)
  *
  * Conventions are those of moe_layer.h: every call returns a moe_status_t
  * (moe_layer_last_error(NULL) describes the calling thread's last failure),

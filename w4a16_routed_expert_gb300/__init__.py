@@ -5,7 +5,8 @@ The layer runs as hand-written CUDA kernels for sm_103a inside
 thin ctypes binding with the same entry-point names and ``layer.MoELayer`` a
 convenience wrapper that takes torch tensors. ``attention.PagedAttention``
 wraps the attention operators that stand beside the layer in a decoder block
-(``include/moe_attention.h``) the same way. ``synth`` draws seeded synthetic
+(``include/moe_attention.h``) and those of a step over trees of drafted tokens
+the same way. ``synth`` draws seeded synthetic
 inputs. Importing this package does not load the library; the binding loads it
 on first use and raises if it has not been built.
 """

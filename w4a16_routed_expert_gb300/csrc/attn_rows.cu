@@ -12,7 +12,11 @@
 // GB), 228 us = 6.7 TB/s, 0.99 of the measured copy rate; 16 behind 4099
 // shared keys with up to 1000 own (92 MB) 25 us: 4 us until the first copy
 // (two dependent loads, then the page's number), 12 us of copies at full rate,
-// 1.5 us to end each part, 4 us for the join.
+// 1.5 us to end each part, 4 us for the join. Trees of drafted tokens: 16 of up
+// to 31 rows of 128 to a key over up to 2600 own keys (175 MB) 40 us, with a
+// prefix of 1000 in the same launch 49; 50 of up to 52 rows of 64 over up to 713
+// (39 MB) 24 us, where the products of mma.sync bind (1019 multiply-adds a cycle
+// and SM, an eighth of tcgen05's).
 //
 // A block is four computing warps and one that copies. Keys and values come
 // page by page as TMA boxes (16 to 64 slots of one head, 128-byte swizzle)

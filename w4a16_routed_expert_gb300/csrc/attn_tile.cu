@@ -16,6 +16,10 @@
 // (64 cycles an MMA), Q K^T, which reads both operands from shared memory, at
 // ~95; the softmax of a row tile takes 1000 to 1300 and hides.
 //
+// Trees of drafted tokens: 8 of 24 to 64 tokens of 8 heads of 128 to a key after
+// up to 30000 keys 183 us (162 GFLOP, 0.46 of the bf16 rate: 27 row tiles for
+// 22.7 rows' worth); 3 of up to 500 tokens of 3 heads of 96 31 us.
+//
 // Warp roles (one block per SM):
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (a warp reaches the 32 lanes of
 //                   tensor memory of its number mod 4); queries in, output out
