@@ -103,7 +103,17 @@ __global__ void __launch_bounds__(kKeepThreads) k_attn_keep(const __grid_constan
   pdl_wait();
   const int tid = threadIdx.x, b = blockIdx.y;
   const int lo = __ldg(a.q_offsets + b), hi = __ldg(a.q_offsets + b + 1), len = __ldg(a.seq_lens + b);
-  int count = __ldg(a.counts + b);
+  const int count = __ldg(a.counts + b);
+  // the path's first words come with the lengths
+  const int32_t* path = a.path + (long long)b * a.path_stride;
+  int p = -1, before = -1;
+  auto ask = [&](int j) {
+    if (tid < kKeepPath && j < a.path_stride) {
+      p = __ldg(path + j);
+      before = j ? __ldg(path + j - 1) : -1;
+    }
+  };
+  ask(tid);
   const int m = max(hi - lo, 0), start = len - m;
   const bool bad = hi < lo || len < 0 || len > a.max_seq_len || count < 0 || count > min(m, a.path_stride) ||
                    (count > 0 && start < 0);
@@ -111,16 +121,16 @@ __global__ void __launch_bounds__(kKeepThreads) k_attn_keep(const __grid_constan
     if (tid == 0) record_error(a.err, kAttnErrBounds);
     return;
   }
-  const int32_t* path = a.path + (long long)b * a.path_stride;
   const int32_t* table = a.block_table + (long long)b * a.table_stride;
   const int d8 = a.D / 8, per = a.Hk * d8, items = a.count * per;
 #pragma unroll 1
   for (int base = 0; base < count; base += kKeepPath) {
     const int here = min(kKeepPath, count - base);
+    if (base) ask(base + tid);
     if (tid == 0) stop = here;
     __syncthreads();
     if (tid < here) {
-      const int j = base + tid, p = __ldg(path + j), before = j ? __ldg(path + j - 1) : -1;
+      const int j = base + tid;
       bool ok = p >= j && p < m && p > before;
       if (ok) {
         auto place = [&](int node, long long* at) {

@@ -12,8 +12,8 @@
 // every block takes the sums over all sequences for itself (at most 4096, a few
 // words a thread) instead of waiting for another, and then its share of the
 // sequences, pages and tokens. The pool's state may be updated in place: the
-// last block to end writes it, when none reads it any more (which costs each
-// block a turn at one counter: 512 prompts of up to 1999 tokens, half a million
+// last block to have read it writes it (which costs each block a turn at one
+// counter: 512 prompts of up to 1999 tokens, half a million
 // in all, take 8.3 us with 304 blocks, 11.3 with 500, 10.3 with 152). Four trees
 // of up to 8 tokens take 4.4 us, 50 of up to 63 7.5.
 #include <algorithm>
@@ -27,14 +27,15 @@ constexpr int kThreads = 256;
 constexpr int kMost = 1 << 30;  // sums stop here
 
 struct SmemPlan {
-  uint32_t off, take, back, served, rows, jump, bytes;
+  uint32_t off, take, back, held, served, rows, jump, bytes;
 };
 __host__ __device__ inline SmemPlan smem_plan(int B, int max_nodes, int words) {
   SmemPlan p;
   p.off = 0;
   p.take = p.off + (uint32_t)(B + 1) * 4;
   p.back = p.take + (uint32_t)(B + 1) * 4;
-  p.served = p.back + (uint32_t)(B + 1) * 4;
+  p.held = p.back + (uint32_t)(B + 1) * 4;
+  p.served = p.held + (uint32_t)B * 4;
   p.rows = (p.served + (uint32_t)B + 3) & ~3u;
   const uint32_t nodes = max_nodes > 32 ? (uint32_t)max_nodes : 0u;
   p.jump = p.rows + nodes * (uint32_t)words * 4;
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   int* off = reinterpret_cast<int*>(smem + sp.off);
   int* take = reinterpret_cast<int*>(smem + sp.take);
   int* back = reinterpret_cast<int*>(smem + sp.back);
+  int* hold = reinterpret_cast<int*>(smem + sp.held);  // pages held before the step
   unsigned char* served = smem + sp.served;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.B, F = a.ring_size;
   pdl_trigger();
@@ -134,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const Ask k = ask(b);
+    hold[b] = a.state[2 + b];
     off[b] = base[0];
     take[b] = base[1];
     back[b] = base[2];
@@ -153,6 +156,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   if (mine) atomicMax(&most_taken, mine);
   if (bad && blockIdx.x == 0) record_error(a.err, kAttnErrBounds);
   __syncthreads();
+  // The old state has been read: this block's turn at the counter, whose answer
+  // is on its way under the rest.
+  unsigned turn = 0;
+  if (tid == 0 && gridDim.x > 1) turn = atom_acq_rel_add(a.ticket, 1u);
   const int taken = most_taken;
   const int given = min(back[B], F - count);
   if (given < back[B] && blockIdx.x == 0 && tid == 0) record_error(a.err, kAttnErrBounds);
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   }
   for (int i = gtid; i < taken; i += grid_threads) {
     const int b = find(take, B, i);
-    a.block_table[(long long)b * a.table_stride + a.state[2 + b] + i - take[b]] = a.free_pages[ring_at(i)];
+    a.block_table[(long long)b * a.table_stride + hold[b] + i - take[b]] = a.free_pages[ring_at(i)];
   }
   for (int i = gtid; i < given; i += grid_threads) {
     const int b = find(back, B, i);
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   };
   auto slot = [&](int b, int key) {
     const int pg = key / a.page_size;
-    return slot_in(page_of(b, a.state[2 + b], pg), key - pg * a.page_size);
+    return slot_in(page_of(b, hold[b], pg), key - pg * a.page_size);
   };
   const int tokens = min(off[B], a.T);
   if (a.max_nodes == 0) {
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
               while (off[b + 1] <= t + i);
             next = off[b + 1];
             ctx = a.context_lens[b];
-            held = a.state[2 + b];
+            held = hold[b];
             ok = served[b];
             pg = -1;
           }
@@ -325,13 +332,13 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
     a.slots[t] = -1;
   }
 
-  // ---- the pool's state, when no block reads the old one any more
-  __syncthreads();
-  if (tid == 0) is_last = gridDim.x == 1 || atom_acq_rel_add(a.ticket, 1u) == gridDim.x - 1;
+  // ---- the pool's state: no block reads the old one any more when the last has
+  // had its turn
+  if (tid == 0) is_last = turn == gridDim.x - 1;
   __syncthreads();
   if (!is_last) return;
   for (int b = tid; b < B; b += kThreads) {
-    const int held = a.state[2 + b];
+    const int held = hold[b];
     a.state_out[2 + b] = served[b] ? held + take[b + 1] - take[b] : back[b + 1] > back[b] ? 0 : held;
   }
   if (tid == 0) {
