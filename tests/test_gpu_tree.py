@@ -190,6 +190,14 @@ TREE = {  # dtype, Hq, Hk, D, page, order, nodes, context, prefix, what a token 
     "many": (F16, 4, 4, 64, 16, "slot", [(3 * i) % 8 for i in range(130)], [(37 * i) % 150 for i in range(130)], 200, "bushy"),
     "fewer keys than tokens": (F16, 4, 4, 64, 16, "slot", [6, 20], [-4, -20], 40, "bushy"),
     "few with fewer keys than tokens": (F16, 2, 2, 128, 16, "slot", [6, 9], [-4, -9], 0, "random"),
+    "whole groups of two row tiles": (BF16, 32, 8, 64, 32, "head", [20 + (7 * i) % 41 for i in range(20)], [(113 * i) % 700 for i in range(20)], 0, "bushy"),
+    "whole groups behind a prefix in front of each": (F16, 32, 8, 128, 48, "head", [33 + (7 * i) % 30 for i in range(20)], [(57 * i) % 300 for i in range(20)], 300, "chain"),
+    "whole groups, some of them empty": (F16, 16, 2, 128, 16, "slot", [20, 0, 33, 0, 7, 64], [0, 0, 5, 90, 400, 127], 0, "random"),
+    "whole groups of one row tile": (BF16, 32, 4, 128, 16, "slot", [8, 5, 8, 3], [400, 900, 0, 333], 0, "bushy"),
+    "whole groups of one row tile and few keys": (F16, 32, 4, 96, 16, "head", [8, 0, 5, 8, 3], [100, 0, 0, 200, 119], 0, "random"),
+    "whole groups with fewer keys than tokens": (F16, 16, 4, 64, 16, "slot", [40, 30, 50], [-40, -7, 20], 200, "bushy"),
+    "whole groups without keys": (F16, 8, 2, 128, 16, "slot", [40, 30], [-40, -30], 0, "random"),
+    "two streams of 64 over many keys": (F16, 64, 4, 64, 16, "slot", [7, 8, 5], [3000, 2100, 900], 0, "chain"),
     "a prefix of many rows beside trees": (BF16, 32, 8, 64, 32, "head", [(3 * i) % 4 for i in range(30)], [(13 * i) % 100 for i in range(30)], 2000, "bushy"),
 }
 

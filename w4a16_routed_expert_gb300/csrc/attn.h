@@ -82,8 +82,9 @@ struct LineArgs {
   float* part_o;         // [rows][DP]: block c's partial of a group stands at the group's first row + c * part_rows
   float2* part_ml;       // [rows] reference maximum (a logit before the scale), sum
   int2 *info_prefix, *info_own;  // [T][Hq] first partial row and number of partials, 0 between forwards
-  int whole;             // not 0: no line; a block takes whole groups of own keys, this many row blocks a sequence,
-                         // and stores their results: nothing is left to join
+  int whole;             // not 0: no line; a block takes whole groups (own keys, `joined` the prefix's before them),
+                         // this many blocks of row_block rows a sequence, and stores their results: nothing is left to
+                         // join
   int final_prefix, final_own;   // 1: these groups' rows have no other partials, one part alone is the result
 };
 // Rows of partial results one kernel can write.

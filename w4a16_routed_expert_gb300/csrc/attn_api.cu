@@ -186,6 +186,60 @@ void fill_rope(const moe_attn* h, moe::RopeArgs* a) {
   a->err = h->err;
 }
 
+// Rows of a block (128 or 256) where over trees the tcgen05 kernel's blocks had
+// better take whole groups of keys, the prefix's in front of every sequence's
+// own, each to its end (LineArgs::whole); 0: better not. That spares a group
+// its parts' ends and the join, which cost more than short trees' products; a
+// line of equal runs makes up for few groups with many keys. By an estimate in
+// us from the most that lengths can be, `tile`: against a line of 256-row
+// groups, else one of the few-row kernel. Whole / in a line, heads of 128:
+//   rows of 128, groups 64, 128, 256: 300 keys 11 / 15, 13 / 16, 23 / 33,
+//   1000 17 / 23, 20 / 32, 35 / 48, 3000 33 / 33, 40 / 51, 76 / 87; 16 groups:
+//   300 keys 11 / 14, 3000 30 / 19
+//   1200 rows of 4 key heads, sequences 1, 3 in blocks of 128, 6, 20 of 256:
+//   500 keys 14 / 17, 15 / 27, 19 / 32, 51 / 71, 1400 19 / 22, 21 / 30, 31 / 45,
+//   82 / 105, 4400 38 / 27, 41 / 47, 69 / 74, 193 / 210
+//   64 rows, few-row kernel, groups 16, 128, 256: 1000 keys 14 / 15, 19 / 29,
+//   34 / 48, 3000 28 / 21, 39 / 55, 74 / 98; whole groups of both, 300 keys: 10 /
+//   14, 12 / 16, 22 / 19. Of 32 rows it is within 15% either way.
+int whole_rows(const moe::AttnArgs& a, int own_rows, int prefix_rows, bool tile, int num_sms) {
+  if (own_rows <= 32 || (!tile && prefix_rows)) return 0;
+  const double rows = (double)a.T * a.g;
+  auto blocks = [&](int block) {  // most row blocks of a sequence
+    return (own_rows + block - 1) / block;
+  };
+  auto groups = [&](int block) {
+    const double even = blocks(block) == 1 ? a.B : 1.05 * (rows / block + 0.5 * a.B);
+    return a.Hk * std::min((double)a.B * blocks(block), even);
+  };
+  auto tiles = [](int keys) { return (double)((keys + moe::kTileKeyTile - 1) / moe::kTileKeyTile); };
+  const double own = tiles(a.max_seq_len), front = prefix_rows ? tiles(a.prefix_len) : 0.0;
+  double line;
+  if (!tile) {
+    if (a.max_seq_len <= moe::kWholeKeys) return a.D > 64 && a.B * a.Hk <= num_sms ? 128 : 0;
+    line = 12.0 + groups(256) * (0.06 + 0.0115 * own) * (a.D > 64 ? 1.0 : 0.5);
+  } else {
+    const bool joined = front && rows >= (double)a.B * moe::kTileRows;
+    const double t = own + (joined ? front : 0.0);
+    line = 15.0 + groups(256) * (own_rows > 128 ? 0.1 + 0.011 * t : std::min(0.02 + 0.013 * t, 0.1 + 0.0065 * t));
+    if (front && !joined) line += 5.0 + a.Hk * std::ceil(rows / moe::kTileRows) * (0.1 + 0.011 * front);
+  }
+  double best = line;
+  int block = 0;
+  for (const int b : {256, 128}) {
+    // (blocks look at every place that a group may have)
+    if ((double)a.B * a.Hk * blocks(b) > 32.0 * num_sms) continue;
+    const bool two = b == 256 && own_rows > 128;
+    const double waves = std::ceil(groups(b) / num_sms);
+    const double us = 4.0 + waves * (two ? 9.0 + 1.56 * (own + front) : 7.0 + 0.95 * (own + front));
+    if (us < best) {
+      best = us;
+      block = b;
+    }
+  }
+  return block;
+}
+
 // Enqueue a forward whose arguments have been checked.
 moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaStream_t s) {
   const bool bf16 = h->cfg.dtype == MOE_DTYPE_BF16;
@@ -199,7 +253,8 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
   const bool over_tree = a.tree != nullptr;
   const int most = moe::rows_most(a.D, over_tree, a.max_seq_len);
   const bool little = own_rows && (long long)a.T * a.Hq * a.prefix_len <= moe::few_triples(over_tree);
-  const bool tile_own = own_rows > most;
+  const int tile_whole = over_tree ? whole_rows(a, own_rows, prefix_rows, own_rows > most, h->num_sms) : 0;
+  const bool tile_own = own_rows > most || tile_whole;
   const bool tile_prefix = prefix_rows && (tile_own || (prefix_rows > most && !little));
   const bool few_own = own_rows && !tile_own, few_prefix = prefix_rows && !tile_prefix;
   // Sequences of a row block and more on average: no block would serve two of
@@ -207,7 +262,7 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
   // instead of two; four chunks of 770 tokens behind 8200 keys: 370 us so, 417
   // apart). The average is what the host knows: a batch of one long chunk and
   // many short ones may pass too, and then reads the prefix for each.
-  const bool joined = tile_own && tile_prefix && (long long)a.T * a.g >= (long long)a.B * moe::kTileRows;
+  const bool joined = tile_own && tile_prefix && (tile_whole || (long long)a.T * a.g >= (long long)a.B * moe::kTileRows);
   moe::JoinArgs j = {};
   j.a = a;
   j.DP = h->DP;
@@ -243,6 +298,11 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
   bool fits = true;
   if (tile_own || tile_prefix)
     fits = line(&tile, moe::kTileRows, moe::kTileKeyTile, moe::kTileWeight, h->num_sms, tile_prefix, tile_own);
+  if (tile_whole) {
+    tile.row_block = tile_whole;
+    tile.whole = (own_rows + tile_whole - 1) / tile_whole;
+    tile.n_cta = (int)std::min<long long>(tile.n_cta, (long long)a.B * a.Hk * tile.whole);
+  }
   if (few_own || few_prefix) {
     // (over trees a prefix takes the own rows' blocks, or blocks of 32: 100
     // sequences of up to 5 rows of 64 behind 2000 keys of 16 heads 70 us, in
@@ -277,7 +337,7 @@ moe_status_t forward(moe_attn* h, const char* fn, const moe::AttnArgs& a, cudaSt
                                                 tile.n_cta && h->pdl, s, h->pdl);
     if (e != cudaSuccess) return failed(e);
   }
-  if (whole) return MOE_OK;
+  if (whole || tile_whole) return MOE_OK;
   const cudaError_t e = moe::launch_attn_join(j, bf16, s, h->pdl);
   return e == cudaSuccess ? MOE_OK : failed(e);
 }

@@ -217,6 +217,58 @@ struct Walk {
   }
 };
 
+// Whole groups instead of a line (LineArgs::whole). What rows that see nothing
+// get, zeros and minus infinity: 16 bytes of them, counted by z from (token,
+// head) on, g heads a token.
+template <typename T>
+__device__ __forceinline__ void store_nothing(const AttnArgs& a, int tok, int head, int g, long long z) {
+  const int r = (int)(z / (a.D / 8)), c8 = (int)(z % (a.D / 8)), t = r / g;
+  const long long at = tok + t;
+  *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.out_stride + (long long)(head + r - t * g) * a.D + c8 * 8) =
+      make_uint4(0, 0, 0, 0);
+  if (a.lse && c8 == 0) a.lse[at * a.Hq + head + r - t * g] = -INFINITY;
+}
+// The tokens behind the last sequence's, by one warp of each block.
+template <typename T>
+__device__ __forceinline__ void clear_behind(const AttnArgs& a, int lane) {
+  const Seq last = load_seq(a, a.B - 1);
+  const int behind = last.t0 + last.n;
+  for (long long z = blockIdx.x * 32 + lane; z < (long long)(a.T - behind) * a.Hq * (a.D / 8); z += gridDim.x * 32)
+    store_nothing<T>(a, behind, 0, a.Hq, z);
+}
+// One warp: the block's next group, of `block` rows at most; false after the
+// last. Rows without keys are stored on the way.
+template <typename T, int KT>
+__device__ __forceinline__ bool next_whole(const AttnArgs& a, const LineArgs& ln, int* group, int block, int lane,
+                                           Segment* s) {
+  const int per = a.Hk * ln.whole;
+  while (*group < a.B * per) {
+    const int b = *group / per, x = *group - b * per, h = x / ln.whole, row0 = (x - h * ln.whole) * block;
+    const Seq q = load_seq(a, b);
+    *group += gridDim.x;
+    const int rows = min(block, q.n * a.g - row0);
+    if (rows <= 0) continue;
+    s->front = front_tiles<KT>(a, ln);
+    s->tiles = s->front + tiles_of<KT>(q.keys);
+    if (s->tiles == 0) {
+      for (int z = row0 * (a.D / 8) + lane; z < (row0 + rows) * (a.D / 8); z += 32)
+        store_nothing<T>(a, q.t0, h * a.g, a.g, z);
+      continue;
+    }
+    s->b = b;
+    s->h = h;
+    s->tile = s->prow = 0;
+    s->row0 = row0;
+    s->rows = rows;
+    s->t0 = q.t0;
+    s->n = q.n;
+    s->klen = s->nkeys = q.keys;
+    s->parts = 1;
+    return true;
+  }
+  return false;
+}
+
 // Whether the part is its rows' whole result, to be stored as it is.
 __device__ __forceinline__ bool whole(const LineArgs& ln, const Segment& s) {
   return s.parts == 1 && (s.b < 0 ? ln.final_prefix : ln.final_own);

@@ -143,50 +143,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     Walk<kKT, RB> w;
     int group = (int)blockIdx.x;
     if (!whole_groups) w.init(a, ln, own_off, own_total);
-    // zeros, and minus infinity: 16 bytes of rows that see nothing, counted from
-    // (token, head) on, g heads a token
-    auto nothing = [&](int tok, int head, int g, long long z) {
-      const int r = (int)(z / (a.D / 8)), c8 = (int)(z % (a.D / 8)), t = r / g;
-      const long long at = tok + t;
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at * a.out_stride + (long long)(head + r - t * g) * a.D + c8 * 8) =
-          make_uint4(0, 0, 0, 0);
-      if (a.lse && c8 == 0) a.lse[at * a.Hq + head + r - t * g] = -INFINITY;
-    };
-    if (whole_groups) {  // tokens behind the last sequence's
-      const Seq last = load_seq(a, a.B - 1);
-      const int behind = last.t0 + last.n;
-      for (long long z = blockIdx.x * 32 + lane; z < (long long)(a.T - behind) * a.Hq * (a.D / 8); z += gridDim.x * 32)
-        nothing(behind, 0, a.Hq, z);
-    }
-    auto next_whole = [&](Segment* s) {
-      while (true) {
-        const int per = a.Hk * ln.whole;
-        if (group >= a.B * per) return false;
-        const int b = group / per, x = group - b * per, h = x / ln.whole, row0 = (x - h * ln.whole) * RB;
-        const Seq q = load_seq(a, b);
-        group += gridDim.x;
-        const int rows = min(RB, q.n * a.g - row0);
-        if (rows <= 0) continue;
-        if (q.keys == 0) {
-          for (int z = row0 * (a.D / 8) + lane; z < (row0 + rows) * (a.D / 8); z += 32) nothing(q.t0, h * a.g, a.g, z);
-          continue;
-        }
-        s->b = b;
-        s->h = h;
-        s->tile = s->front = s->prow = 0;
-        s->tiles = tiles_of<kKT>(q.keys);
-        s->row0 = row0;
-        s->rows = rows;
-        s->t0 = q.t0;
-        s->n = q.n;
-        s->klen = s->nkeys = q.keys;
-        s->parts = 1;
-        return true;
-      }
-    };
+    if (whole_groups) clear_behind<T>(a, lane);
     while (ok) {
       Segment s;
-      const bool some = whole_groups ? next_whole(&s) : w.next(a, ln, own_off, &s);
+      const bool some = whole_groups ? next_whole<T, kKT>(a, ln, &group, RB, lane, &s) : w.next(a, ln, own_off, &s);
       if (!some) {
         s.tiles = 0;
         s.tile = s.b = s.nkeys = s.front = 0;  // no page to ask for

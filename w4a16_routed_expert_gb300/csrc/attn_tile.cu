@@ -17,14 +17,18 @@
 // ~95; the softmax of a row tile takes 1000 to 1300 and hides.
 //
 // Trees of drafted tokens: 8 of 24 to 64 tokens of 8 heads of 128 to a key after
-// up to 30000 keys 183 us (162 GFLOP, 0.46 of the bf16 rate: 27 row tiles for
-// 22.7 rows' worth); 3 of up to 500 tokens of 3 heads of 96 31 us.
+// up to 30000 keys 178 us (162 GFLOP, 0.48 of the bf16 rate: 27 row tiles for
+// 22.7 rows' worth). Where lengths are short blocks take whole groups and store
+// results (LineArgs::whole, whole_rows in attn_api.cu): 3 of up to 500 tokens of
+// 3 heads of 96 behind 300 keys 24 us, 31 in a line; 32 of 128 rows of 8 key heads
+// after 1000 keys 35, 48.
 //
 // Warp roles (one block per SM):
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (a warp reaches the 32 lanes of
 //                   tensor memory of its number mod 4); queries in, output out
 //   warp 8          TMA: pages to shared memory, 128-byte swizzle, keys and
 //                   values in turn through one ring
+//   warp 11         (kTwoCopy) the values in warp 8's place
 //   warp 9          tensor memory and the MMAs, issued by one elected lane:
 //                   P V of a key tile, then the next Q K^T of the same rows,
 //                   row tiles in turn, so that one's products run under the
@@ -49,8 +53,21 @@ namespace moe {
 namespace {
 
 constexpr int kKT = kTileKeyTile;
-constexpr int kThreads = 11 * 32;
-constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLanded = 10;
+// Over trees of heads above 64 elements a warp of its own copies the values: a
+// box of a page takes ~85 cycles to issue, and with pages of 16 slots (or 48)
+// one warp's 32 boxes a key tile take longer than its products (four trees of
+// 500 to 1000 tokens behind 8200 keys in pages of 48: 391 us, 462 with one copying
+// warp; 8 trees after up to 30000 keys in pages of 64: 178, 184). Heads to 64
+// have half of the boxes (16000 keys for 350 tokens: 98 us, 100 with it).
+//
+// A stage's phases stay in step although two warps fill the ring: what either
+// waits for is at most one use of the stage away, because stages are given back
+// in order and neither skips more than two of the four or more that there are.
+template <bool TREE, int DP>
+constexpr bool kTwoCopy = TREE && DP == 128;
+template <bool TREE, int DP>
+constexpr int kThreadsOf = (kTwoCopy<TREE, DP> ? 12 : 11) * 32;
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLanded = 10, kWarpValues = 11;
 constexpr int kMaxStages = 8;
 // A row's weights of one tile: a reference at the maximum gives at most 128 *
 // 2^7 (FP16, ProbBias), and below 2^15 no FP16 weight overflows.
@@ -65,7 +82,7 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
   p.bars = p.ring + (uint32_t)stages * kKT * DP * 2;
   p.seg = p.bars + (2 * (kMaxStages + kSegSlots) + 19) * 8;
   p.misc = p.seg + kSegSlots * sizeof(Segment);
-  p.off = p.misc + 80;
+  p.off = p.misc + 96;
   p.bytes = p.off + (uint32_t)(B + 1) * 4;
   return p;
 }
@@ -73,11 +90,22 @@ __host__ __device__ inline SmemPlan smem_plan(int DP, int stages, int B) {
 struct Misc {
   uint32_t tmem;
   int abort_flag;
-  int issued;  // stages handed to TMA
   int mma_issued;
-  int32_t scratch[12];
+  int32_t phase[kMaxStages];  // of the stage's last copy, -1: none
+  int32_t scratch[kThreadsOf<true, 128> / 32];
 };
-static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
+static_assert(sizeof(Misc) <= 96, "SmemPlan's room for Misc");
+
+// With twelve warps a thread has 168 registers at launch; the four that do not
+// work on logits hand theirs on: 4 x 104 + 8 x 200 = 12 x 168.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // RSUM: the quotient takes the sum of the weights as they were rounded for the
 // products (few rows, see launch_attn_tile). TREE: a token sees of its
@@ -91,12 +119,13 @@ static_assert(sizeof(Misc) <= 80, "SmemPlan's room for Misc");
 // such parts (8 sequences of 15000 keys, 128 rows of 128 to a key: 88 us, 98 with
 // one stream; 1024 groups of 128 rows and up to 228 keys: 71).
 template <typename T, int DP, bool RSUM, bool TREE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   constexpr int NH = DP / 64;
+  constexpr bool kTwo = kTwoCopy<TREE, DP>;
   constexpr bool kBf16 = sizeof(T) == 2 && ProbBias<T>::value == 0.f;
   // Head sizes to 64 leave room for a third S tile: the next key tile's Q K^T is
   // issued before a row tile's probabilities are in, S_t(j) in place (2 j + t)
@@ -130,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
+      misc->phase[i] = -1;
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -143,14 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 10);  // eight softmax warps, kWarpMma, kWarpLanded
+      mbar_init(&seg_empty[i], kTwo ? 11 : 10);  // eight softmax warps, kWarpMma, kWarpLanded, kWarpValues
     }
     mbar_init(drain, 1);
     mbar_init(d_full, 1);
     mbar_init(ml_full, 8);
     mbar_init(o_read, 4);
     misc->abort_flag = 0;
-    misc->issued = 0;
     misc->mma_issued = 0;
     fence_mbar_init();
   }
@@ -163,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // only now: a kernel that starts on this trigger and does not wait itself
   // may rely on everything before this launch
   pdl_trigger();
-  const int own_total = scan_own<kThreads, kKT, kTileRows>(a, ln, own_off, misc->scratch);
+  const bool whole_groups = TREE && ln.whole;
+  const int own_total = whole_groups ? 0 : scan_own<kThreadsOf<TREE, DP>, kKT, kTileRows>(a, ln, own_off, misc->scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -171,26 +201,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto is_dual = [](const Segment& s) { return TREE && s.rows <= 128 && s.tiles > 1; };
 
   if (warp >= kWarpCopy) {
-  if (warp == kWarpCopy) {
+  if (kTwo) setmaxnreg_dec<104>();
+  if (warp == kWarpCopy || (kTwo && warp == kWarpValues)) {
     // ------------------------------------------------ the walk and its copies
-    // lane (box, half of the head): one box of every key and value tile
+    // lane (box, half of the head): one box of every tile of this warp's
+    const bool vals = kTwo && warp == kWarpValues;
     const int c = lane / NH, hf = lane % NH;
     const int box = 1 << box_log2;
     const bool mine = c < (kKT >> box_log2);
     const bool split = (a.D & 63) != 0;
     const int cx = split ? hf * 64 : 0, ch = split ? 0 : hf;
     const uint32_t dst0 = smem_u32(smem) + sp.ring + (uint32_t)hf * kHalf + (uint32_t)c * box * 128;
-    int st = 0, issued = 0, slot_i = 0;
+    int st = 0, slot_i = 0;
     uint32_t ph = 0, sph = 0;
     bool ok = true;
     Walk<kKT, kTileRows> w;
-    w.init(a, ln, own_off, own_total);
+    int group = (int)blockIdx.x;
+    if (!vals && whole_groups) clear_behind<T>(a, lane);
+    if (!vals && !whole_groups) w.init(a, ln, own_off, own_total);
     while (ok) {
       Segment s;
-      const bool some = w.next(a, ln, own_off, &s);
-      if (!some) {
-        s.tiles = 0;
-        s.tile = s.b = s.nkeys = s.front = 0;  // no page to ask for
+      if (vals) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&seg_full[slot_i], sph, abort_flag, a.err));
+        if (!ok) break;
+        s = segs[slot_i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[slot_i]);
+      } else {
+        const bool some =
+            whole_groups ? next_whole<T, kKT>(a, ln, &group, ln.row_block, lane, &s) : w.next(a, ln, own_off, &s);
+        if (!some) {
+          s.tiles = 0;
+          s.tile = s.b = s.nkeys = s.front = 0;  // no page to ask for
+        }
       }
       const int32_t* own = s.b < 0 ? a.prefix_pages : a.block_table + (long long)s.b * a.table_stride;
       int slot = 0;  // of the page, of the lane's box of the current tile
@@ -207,56 +250,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot = key - pg * a.page_size;
         return __ldg((pre ? a.prefix_pages : own) + pg);  // looked at (page_in_cache) when it is used, not before
       };
-      auto issue = [&](const CUtensorMap* tm, bool some_keys, int page, int at, int boxes) {
+      int z = 0;  // place in the part's order of copies
+      auto to = [&](int y) {  // (at most three stages on: there are four)
+        if ((st += y - z) >= stages) {
+          st -= stages;
+          ph ^= 1u;
+        }
+        z = y;
+      };
+      auto issue = [&](const CUtensorMap* tm, int y, bool some_keys, int page, int at, int boxes) {
+        to(y);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
+        if (lane == 0) {
+          misc->phase[st] = (int)ph;
+          mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
+        }
         __syncwarp();
         if (some_keys)
           tma_load_5d(dst0 + (uint32_t)st * kTileBytes, tm, cx, at, ch, s.h, page_in_cache(a, page), &full[st]);
-        ++issued;
-        if (++st == stages) {
-          st = 0;
-          ph ^= 1u;
-        }
       };
-      // keys and values in turn, with kAhead or two streams the next tile's keys before a
-      // tile's values: the order in which the MMA warp comes to them
       int page = page_of(s.tile);
       // (the first page's number is on its way meanwhile)
-      ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
-      if (!ok) break;
-      if (lane == 0) {
-        segs[slot_i] = s;
-        mbar_arrive(&seg_full[slot_i]);
+      if (!vals) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&seg_empty[slot_i], sph ^ 1u, abort_flag, a.err));
+        if (!ok) break;
+        if (lane == 0) {
+          segs[slot_i] = s;
+          mbar_arrive(&seg_full[slot_i]);
+        }
       }
       if (++slot_i == kSegSlots) {
         slot_i = 0;
         sph ^= 1u;
       }
-      if (!some) break;
-      int vpage = 0, vat = 0, vboxes = 0;
-      bool vhave = false;
+      if (s.tiles == 0) break;
+      // keys and values in turn, with kAhead or two streams the next tile's keys before a
+      // tile's values: the order in which the MMA warp comes to them
       const bool ahead = kAhead || is_dual(s);
+      if constexpr (kTwo) {
+        const CUtensorMap* tm = vals ? &tv : &tk;
 #pragma unroll 1
-      for (int i = 0; i < s.tiles + (ahead ? 1 : 0) && ok; ++i) {
-        const int at = slot, boxes = (here + box - 1) >> box_log2;
-        const bool has = have;
-        const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : 0;
-        if (i < s.tiles) issue(&tk, has, page, at, boxes);
-        if (!ahead) {
-          if (ok) issue(&tv, has, page, at, boxes);
-        } else {
-          if (ok && i > 0) issue(&tv, vhave, vpage, vat, vboxes);
-          vhave = has;
-          vpage = page;
-          vat = at;
-          vboxes = boxes;
+        for (int i = 0; i < s.tiles && ok; ++i) {
+          const int at = slot, boxes = (here + box - 1) >> box_log2, now = page;
+          const bool has = have;
+          if (i + 1 < s.tiles) page = page_of(s.tile + i + 1);
+          issue(tm, vals ? 2 * i + (ahead && i + 1 < s.tiles ? 2 : 1) : 2 * i - (ahead && i > 0 ? 1 : 0), has, now, at,
+                boxes);
         }
-        page = next;
+      } else {
+        int vpage = 0, vat = 0, vboxes = 0;
+        bool vhave = false;
+#pragma unroll 1
+        for (int i = 0; i < s.tiles + (ahead ? 1 : 0) && ok; ++i) {
+          const int at = slot, boxes = (here + box - 1) >> box_log2;
+          const bool has = have;
+          const int next = i + 1 < s.tiles ? page_of(s.tile + i + 1) : 0;
+          if (i < s.tiles) issue(&tk, ahead && i > 0 ? 2 * i - 1 : 2 * i, has, page, at, boxes);
+          if (!ahead) {
+            if (ok) issue(&tv, 2 * i + 1, has, page, at, boxes);
+          } else {
+            if (ok && i > 0) issue(&tv, i < s.tiles ? 2 * i : 2 * i - 1, vhave, vpage, vat, vboxes);
+            vhave = has;
+            vpage = page;
+            vat = at;
+            vboxes = boxes;
+          }
+          page = next;
+        }
       }
+      to(2 * s.tiles);
     }
-    if (lane == 0) misc->issued = issued;
   } else if (warp == kWarpMma) {
     // ----------------------------------------------------------------- MMA
     {
@@ -470,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ------------------------------------------------------------- softmax
+    if (kTwo) setmaxnreg_inc<200>();
     const int t = warp >> 2;                       // row tile
     const int r_lane = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -790,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ln.part_ml[cur->prow + r] = make_float2(m, l);
             else if (a.lse)
               a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(m, l, a.scale);
-            if (cur->parts) write_info(a, ln, *cur, r, at);
+            if (cur->parts && !whole_groups) write_info(a, ln, *cur, r, at);
           }
         }
         tc_fence_before();
@@ -854,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ln.part_ml[cur->prow + r] = make_float2(mref, l);
             else if (a.lse)
               a.lse[(long long)at.x * a.Hq + at.y] = log_sum<T>(mref, l, a.scale);
-            if (cur->parts) write_info(a, ln, *cur, r, at);
+            if (cur->parts && !whole_groups) write_info(a, ln, *cur, r, at);
           }
         }
         tc_fence_before();
@@ -875,9 +940,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (misc->abort_flag) {
     // a block that gave up lets its copies and MMAs end before it leaves
     if (warp == kWarpCopy && lane == 0) {
-      const int n = misc->issued;
-      for (int i = 0; i < stages && i < n; ++i)
-        mbar_wait(&full[i], (uint32_t)((n - 1 - i) / stages) & 1u, nullptr, nullptr);
+      for (int i = 0; i < stages; ++i)
+        if (misc->phase[i] >= 0) mbar_wait(&full[i], (uint32_t)misc->phase[i], nullptr, nullptr);
     }
     if (warp == kWarpMma && misc->mma_issued) {
       commit_elect(elect_one(), drain);  // the lane that issued the MMAs
@@ -897,7 +961,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
   const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
   const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE>, smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreads), smem, s, pdl, tk, tv, a, ln, stages,
+  return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreadsOf<TREE, DP>), smem, s, pdl, tk, tv, a, ln, stages,
                    box_log2);
 }
 
