@@ -14,8 +14,9 @@
 // sequences, pages and tokens. The pool's state may be updated in place: the
 // last block to have read it writes it (which costs each block a turn at one
 // counter: 512 prompts of up to 1999 tokens, half a million
-// in all, take 8.3 us with 304 blocks, 11.3 with 500, 10.3 with 152). Four trees
-// of up to 8 tokens take 4.4 us, 50 of up to 63 7.5.
+// in all, take 7.9 us with 304 blocks; before the pool's state was read
+// once 8.3, then 11.3 with 500, 10.3 with 152). Four trees
+// of up to 8 tokens take 4.3 us, 50 of up to 63 7.4.
 #include <algorithm>
 
 #include "attn_dev.cuh"
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   const int tokens = min(off[B], a.T);
   if (a.max_nodes == 0) {
     // lines: four tokens a thread, mostly of one sequence and one page (512
-    // prompts of up to 1999 tokens: 8.3 us, 11.0 with one)
+    // prompts of up to 1999 tokens: 7.9 us, 11.0 with one)
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
     for (int t = gtid * 4; t < tokens; t += grid_threads * 4) {
       const int n = min(4, tokens - t);
