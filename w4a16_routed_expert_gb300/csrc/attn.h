@@ -119,7 +119,8 @@ bool encode_cache_map(CUtensorMap* tm, const void* cache, bool bf16, int D, int 
 // Over trees up to 64, the warps as 1 by 4, 2 by 2 or 4 by 1 groups of 16 rows
 // and of keys, at head sizes above 64 up to 32 where contexts may be long: 16
 // trees of 64 rows of 128 to a key after 100, 500, 2000 keys 18, 32, 62 us (24,
-// 35, 59 on the tcgen05 tiles), 64 trees after 100 keys 52 (70), but 8 after
+// 35, 59 on the tcgen05 tiles in a line; in whole groups, which 33 rows and more
+// may take, see whole_rows in attn_api.cu), 64 trees after 100 keys 52 (70), but 8 after
 // 15000 keys 107 (86): there the products bind. 128 rows after 500 keys 57 (39).
 constexpr int kRowsMax = 64;
 constexpr int kRowsLong = 4096;  // own keys

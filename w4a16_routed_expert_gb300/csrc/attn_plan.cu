@@ -13,10 +13,10 @@
 // words a thread) instead of waiting for another, and then its share of the
 // sequences, pages and tokens. The pool's state may be updated in place: the
 // last block to have read it writes it (which costs each block a turn at one
-// counter: 512 prompts of up to 1999 tokens, half a million
-// in all, take 7.9 us with 304 blocks; before the pool's state was read
-// once 8.3, then 11.3 with 500, 10.3 with 152). Four trees
-// of up to 8 tokens take 4.3 us, 50 of up to 63 7.4.
+// counter: 512 prompts of up to 1999 tokens, half a million in all, take 7.9 us
+// with 304 blocks; where each block read the state twice 8.3, and then 11.3 with
+// 500, 10.3 with 152). Four trees of up to 8 tokens take 4.3 us, 50 of up to 63
+// 7.4.
 #include <algorithm>
 
 #include "attn_dev.cuh"

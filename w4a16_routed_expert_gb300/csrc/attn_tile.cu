@@ -58,7 +58,7 @@ constexpr int kKT = kTileKeyTile;
 // one warp's 32 boxes a key tile take longer than its products (four trees of
 // 500 to 1000 tokens behind 8200 keys in pages of 48: 391 us, 462 with one copying
 // warp; 8 trees after up to 30000 keys in pages of 64: 178, 184). Heads to 64
-// have half of the boxes (16000 keys for 350 tokens: 98 us, 100 with it).
+// have half of the boxes (16000 keys for 350 tokens: 95 us, 100 with it).
 //
 // A stage's phases stay in step although two warps fill the ring: what either
 // waits for is at most one use of the stage away, because stages are given back
@@ -118,7 +118,11 @@ __device__ __forceinline__ void setmaxnreg_inc() {
 // tiles, and the streams' sums are joined where the part ends. Trees mostly have
 // such parts (8 sequences of 15000 keys, 128 rows of 128 to a key: 88 us, 98 with
 // one stream; 1024 groups of 128 rows and up to 228 keys: 71).
-template <typename T, int DP, bool RSUM, bool TREE>
+// WHOLE: LineArgs::whole at head sizes to 64, a kernel of its own; above, one
+// kernel does both. Measured so: 350 tokens over 16000 keys of 64, in a line, 95
+// us apart, 98 in one; 8 trees of 128 after up to 30000 keys 183 apart, 178 in
+// one; chunks in pages of 48 415, 391 (the code is the same but for the branch).
+template <typename T, int DP, bool RSUM, bool TREE, bool WHOLE>
 __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
     k_attn_tile(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,
                 const LineArgs ln, int stages, int box_log2) {
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
   // only now: a kernel that starts on this trigger and does not wait itself
   // may rely on everything before this launch
   pdl_trigger();
-  const bool whole_groups = TREE && ln.whole;
+  const bool whole_groups = WHOLE || (kTwo && ln.whole);
   const int own_total = whole_groups ? 0 : scan_own<kThreadsOf<TREE, DP>, kKT, kTileRows>(a, ln, own_off, misc->scratch);
   tc_fence_before();
   __syncthreads();
@@ -953,15 +957,15 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP, bool RSUM, bool TREE>
+template <typename T, int DP, bool RSUM, bool TREE, bool WHOLE>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int box_log2,
                    cudaStream_t s, bool pdl) {
   int stages = kMaxStages;  // as many as fit
   while (stages > 2 && smem_plan(DP, stages, a.B).bytes + 1024 > 227 * 1024) --stages;
   const size_t smem = smem_plan(DP, stages, a.B).bytes + 1024;
-  const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE>, smem);
+  const cudaError_t e = ensure_smem(k_attn_tile<T, DP, RSUM, TREE, WHOLE>, smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k_attn_tile<T, DP, RSUM, TREE>, dim3(ln.n_cta), dim3(kThreadsOf<TREE, DP>), smem, s, pdl, tk, tv, a, ln, stages,
+  return launch_ex(k_attn_tile<T, DP, RSUM, TREE, WHOLE>, dim3(ln.n_cta), dim3(kThreadsOf<TREE, DP>), smem, s, pdl, tk, tv, a, ln, stages,
                    box_log2);
 }
 
@@ -971,15 +975,15 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs&
 // hundred keys, up to 1.8 times, or 1.4 with the quotient by the rounded sum,
 // which costs about 10% (four chunks of 770 tokens 406 us against 370, 64
 // sequences behind 32768 keys 92 against 83). Below 4096 rows it is taken.
-template <typename T, bool TREE>
+template <typename T, bool TREE, bool WHOLE>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, const LineArgs& ln, int bl,
                      cudaStream_t s, bool pdl) {
   const bool few = (long long)a.T * a.Hq < 4096;
   if (a.D <= 64)
-    return few ? launch<T, 64, true, TREE>(tk, tv, a, ln, bl, s, pdl)
-               : launch<T, 64, false, TREE>(tk, tv, a, ln, bl, s, pdl);
-  return few ? launch<T, 128, true, TREE>(tk, tv, a, ln, bl, s, pdl)
-             : launch<T, 128, false, TREE>(tk, tv, a, ln, bl, s, pdl);
+    return few ? launch<T, 64, true, TREE, WHOLE>(tk, tv, a, ln, bl, s, pdl)
+               : launch<T, 64, false, TREE, WHOLE>(tk, tv, a, ln, bl, s, pdl);
+  return few ? launch<T, 128, true, TREE, false>(tk, tv, a, ln, bl, s, pdl)
+             : launch<T, 128, false, TREE, false>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace
@@ -988,11 +992,14 @@ cudaError_t launch_attn_tile(const CUtensorMap& tk, const CUtensorMap& tv, const
                              int box_slots, bool bf16, cudaStream_t s, bool pdl) {
   int bl = 4;
   while ((1 << bl) < box_slots) ++bl;
+  if (ln.whole && a.D <= 64)
+    return bf16 ? launch_t<__nv_bfloat16, true, true>(tk, tv, a, ln, bl, s, pdl)
+                : launch_t<__half, true, true>(tk, tv, a, ln, bl, s, pdl);
   if (a.tree)
-    return bf16 ? launch_t<__nv_bfloat16, true>(tk, tv, a, ln, bl, s, pdl)
-                : launch_t<__half, true>(tk, tv, a, ln, bl, s, pdl);
-  return bf16 ? launch_t<__nv_bfloat16, false>(tk, tv, a, ln, bl, s, pdl)
-              : launch_t<__half, false>(tk, tv, a, ln, bl, s, pdl);
+    return bf16 ? launch_t<__nv_bfloat16, true, false>(tk, tv, a, ln, bl, s, pdl)
+                : launch_t<__half, true, false>(tk, tv, a, ln, bl, s, pdl);
+  return bf16 ? launch_t<__nv_bfloat16, false, false>(tk, tv, a, ln, bl, s, pdl)
+              : launch_t<__half, false, false>(tk, tv, a, ln, bl, s, pdl);
 }
 
 }  // namespace moe
