@@ -1,0 +1,52 @@
+"""The operators around drafted trees at the edges of what their declarations
+allow: lengths far out of range, rows of wider arrays."""
+import ctypes
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+from test_gpu_attention import F16, _cuda, caches  # noqa: E402,F401
+from w4a16_routed_expert_gb300 import capi  # noqa: E402
+from w4a16_routed_expert_gb300.attention import PagedAttention  # noqa: E402
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("T,B,nodes", [(1 << 22, 1793, 0), (1 << 22, 2048, 64), (1 << 21, 4096, 0), ((1 << 22) - 1, 4096, 32)])
+def test_plan_of_lengths_far_out_of_range_stays_in_its_outputs(T, B, nodes):
+    """More tokens than room, in every sequence, as memory that was not filled
+    may hold: recorded, none served, nothing stored beside the outputs."""
+    kc, vc = caches(4, 16, 1, 8, F16, "slot", fill=0.0)
+    a = PagedAttention(num_q_heads=1, num_kv_heads=1, head_dim=8, k_cache=kc, v_cache=vc)
+    words, guard = -(-nodes // 32), 1 << 16
+    sizes = dict(q_offsets=B + 1, seq_lens=B, positions=T, slots=T, tree=T * words)
+    sizes = {k: n for k, n in sizes.items() if n}
+    buf = torch.full((sum(-(-n // 4) * 4 + guard for n in sizes.values()) + guard,), -5, dtype=torch.int32, device="cuda")
+    at, out, mine = guard, {}, torch.zeros(buf.numel(), dtype=torch.bool, device="cuda")
+    for name, n in sizes.items():
+        out[name] = buf[at:at + n]
+        mine[at:at + n] = True
+        at += -(-n // 4) * 4 + guard
+    ctx, new = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    parents = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    table, ring, state = ints([[0, 1]] * B), ints([0, 1, 2, 3]), ints([0, 4] + [0] * B)
+    p = capi.moe_attn_plan_t(num_seqs=B, num_tokens=T, max_nodes=nodes, prefix_len=3, context_lens=ctx.data_ptr(), new_lens=new.data_ptr(),
+                             parents=parents.data_ptr() if nodes else None, block_table=table.data_ptr(), table_stride=2, free_capacity=4,
+                             free_pages=ring.data_ptr(), state=state.data_ptr(), state_out=state.data_ptr(),
+                             **{k: t.data_ptr() for k, t in out.items()})
+    s = torch.cuda.current_stream().cuda_stream
+    assert capi.lib().moe_attn_plan(a.handle, ctypes.byref(p), s) == capi.MOE_OK
+    with pytest.raises(capi.MoEError) as e:
+        a.sync()
+    assert e.value.status == capi.MOE_ERR_INVALID_ARG
+    assert out["q_offsets"].tolist() == [min(b * (T + 1), T) for b in range(B + 1)]
+    assert (out["seq_lens"] == 0).all() and (out["slots"] == -1).all()
+    assert not nodes or (out["tree"] == 0).all()  # a tree of more than max_nodes
+    assert (buf[~mine] == -5).all()
+    assert state.tolist() == [0, 4] + [0] * B and ring.tolist() == [0, 1, 2, 3] and (table == ints([0, 1])).all()

@@ -20,12 +20,12 @@
 #include <algorithm>
 
 #include "attn_dev.cuh"
+#include "attn_plan.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMost = 1 << 30;  // sums stop here
 
 struct SmemPlan {
   uint32_t off, take, back, held, served, rows, jump, bytes;
@@ -44,25 +44,8 @@ __host__ __device__ inline SmemPlan smem_plan(int B, int max_nodes, int words) {
   return p;
 }
 
-__device__ __forceinline__ int add_most(int x, int y) { return min(x + y, kMost); }
-
-// What a sequence asks for.
-struct Ask {
-  int m;     // tokens
-  int need;  // pages beyond those it holds
-  int back;  // pages it gives back
-  bool valid;
-};
-__device__ __forceinline__ Ask ask_of(const PlanArgs& a, int ctx, int fresh, int held) {
-  Ask k;
-  const long long keys = (long long)ctx + max(fresh, 0);
-  k.valid = fresh >= -1 && held >= 0 && held <= a.table_stride &&
-            (fresh < 0 || (ctx >= 0 && keys <= min((long long)a.table_stride * a.page_size, 1LL << 30))) &&
-            (a.max_nodes == 0 || fresh <= a.max_nodes);
-  k.m = min(max(fresh, 0), a.T + 1);
-  k.need = k.valid && fresh >= 0 ? max(0, (int)((keys + a.page_size - 1) / a.page_size) - held) : 0;
-  k.back = k.valid && fresh < 0 ? held : 0;
-  return k;
+__device__ __forceinline__ PlanAsk ask_of(const PlanArgs& a, int ctx, int fresh, int held) {
+  return plan_ask(a.T, a.max_nodes, a.table_stride, a.page_size, ctx, fresh, held);
 }
 
 // The last b with at[b] <= x; at ascends, at[0] = 0.
@@ -103,10 +86,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
   if (tid == 0) most_taken = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const Ask k = ask(b);
-    sum[0] = add_most(sum[0], k.m);
-    sum[1] = add_most(sum[1], k.need);
-    sum[2] = add_most(sum[2], k.back);
+    const PlanAsk k = ask(b);
+    sum[0] = plan_add(sum[0], k.m);
+    sum[1] = plan_add(sum[1], k.need);
+    sum[2] = plan_add(sum[2], k.back);
     bad |= !k.valid;
   }
   int incl[3];
@@ -116,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl[i], o);
-      if (lane >= o) incl[i] = add_most(incl[i], y);
+      if (lane >= o) incl[i] = plan_add(incl[i], y);
     }
     if (lane == 31) part[i][warp] = incl[i];
   }
@@ -129,21 +112,21 @@ __global__ void __launch_bounds__(kThreads) k_attn_plan(const PlanArgs a) {
     total[i] = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) base[i] = add_most(base[i], part[i][w]);
-      total[i] = add_most(total[i], part[i][w]);
+      if (w < warp) base[i] = plan_add(base[i], part[i][w]);
+      total[i] = plan_add(total[i], part[i][w]);
     }
   }
   int mine = 0;  // pages taken up to this thread's last sequence that is served
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const Ask k = ask(b);
+    const PlanAsk k = ask(b);
     hold[b] = a.state[2 + b];
     off[b] = base[0];
     take[b] = base[1];
     back[b] = base[2];
     const bool room = base[0] + k.m <= a.T;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) base[i] = add_most(base[i], i == 0 ? k.m : i == 1 ? k.need : k.back);
+    for (int i = 0; i < 3; ++i) base[i] = plan_add(base[i], i == 0 ? k.m : i == 1 ? k.need : k.back);
     const bool ok = k.valid && a.new_lens[b] >= 0 && room && (k.need == 0 || base[1] <= count);
     served[b] = ok;
     if (ok && k.need) mine = base[1];
