@@ -183,8 +183,9 @@ moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride,
  * is seen by all; batch->causal is not looked at. A step may be padded: tokens
  * behind the last sequence's change nothing in the others' rows; their own get
  * zeros, or behind a prefix nothing of use.
- *   tree         device [T][tree_stride]
- *   tree_stride  words of a token, at least max_q_len / 32 rounded up;
+ *   tree         device [T], rows of W = max_q_len / 32 rounded up words; none
+ *                behind a row's first W is read
+ *   tree_stride  words from one token's row to the next, at least W;
  *                T * tree_stride below 2^31
  * NULL with max_seq_len 0 (there are no own keys). */
 moe_status_t moe_attn_forward_tree(moe_attn_t* attn, const void* q, int64_t q_stride, const moe_attn_batch_t* batch,

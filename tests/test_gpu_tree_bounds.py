@@ -9,7 +9,10 @@ torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
 
-from test_gpu_attention import F16, _cuda, caches  # noqa: E402,F401
+import numpy as np  # noqa: E402
+
+import tree_oracle as TO  # noqa: E402
+from test_gpu_attention import F16, _cuda, build, caches  # noqa: E402,F401
 from w4a16_routed_expert_gb300 import capi  # noqa: E402
 from w4a16_routed_expert_gb300.attention import PagedAttention  # noqa: E402
 
@@ -50,3 +53,16 @@ def test_plan_of_lengths_far_out_of_range_stays_in_its_outputs(T, B, nodes):
     assert not nodes or (out["tree"] == 0).all()  # a tree of more than max_nodes
     assert (buf[~mine] == -5).all()
     assert state.tolist() == [0, 4] + [0] * B and ring.tolist() == [0, 1, 2, 3] and (table == ints([0, 1])).all()
+
+
+@pytest.mark.parametrize("D,Hq,nodes,context", [(64, 2, [5, 13], [20, 200]), (128, 2, [31, 17], [400, 3]), (64, 4, [90, 40], [33, 500])])
+def test_a_tree_in_the_last_columns_of_a_wider_array(D, Hq, nodes, context):
+    """The last token's words are the array's last ones."""
+    a, q, _, _, args = build(F16, Hq, 2, D, 16, "slot", nodes, [c + m for c, m in zip(context, nodes)], 0, seed=3)
+    words = -(-max(nodes) // 32)
+    bits = torch.cat([TO.pack(TO.branches(TO.random_tree(np.random.default_rng(4), m, "bushy")), words) for m in nodes]).cuda()
+    wide = torch.full((bits.shape[0], words + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, 3:] = bits
+    want = a.forward(q.cuda(), tree=bits, **args)
+    assert torch.equal(a.forward(q.cuda(), tree=wide[:, 3:], **args), want)
+    a.sync()

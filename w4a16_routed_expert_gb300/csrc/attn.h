@@ -49,8 +49,8 @@ struct AttnArgs {
   int T, B, Hq, Hk, g, D;
   const int32_t *q_offsets, *seq_lens, *block_table, *prefix_pages;
   int table_stride, prefix_len, causal, max_q_len, max_seq_len;
-  const uint32_t* tree;  // nullable: [T][tree_words], bit j of a token's row: it sees its sequence's token j (causal is 0)
-  int tree_words;
+  const uint32_t* tree;  // nullable: a row of bits a token, bit j: it sees its sequence's token j (causal is 0)
+  int tree_words, tree_stride;  // words of a row that are read; from one row to the next
   float scale;           // of the logits
   void* out;
   long long out_stride;

@@ -10,6 +10,7 @@
 #include <new>
 
 #include "attn.h"
+#include "attn_tree.h"
 #include "layer_internal.h"
 #include "moe_attention.h"
 
@@ -379,7 +380,7 @@ moe_status_t forward_call(moe_attn* h, const char* fn, const void* q, int64_t q_
   if (over_tree && b->max_seq_len > 0) {
     if (!tree || reinterpret_cast<uintptr_t>(tree) % 4)
       return set_error(MOE_ERR_INVALID_ARG, "%s: tree must be 4-byte aligned and not NULL", fn);
-    if (tree_stride < (b->max_q_len + 31) / 32 || (long long)tree_stride * b->num_tokens > INT_MAX)
+    if (tree_stride < moe::tree_row_words(b->max_q_len) || (long long)tree_stride * b->num_tokens > INT_MAX)
       return set_error(MOE_ERR_INVALID_ARG, "%s: tree_stride=%d: at least max_q_len / 32, num_tokens * it below 2^31", fn,
                        tree_stride);
   }
@@ -411,7 +412,8 @@ moe_status_t forward_call(moe_attn* h, const char* fn, const void* q, int64_t q_
   a.causal = over_tree ? 0 : b->causal;
   if (over_tree && b->max_seq_len > 0) {
     a.tree = tree;
-    a.tree_words = tree_stride;
+    a.tree_words = moe::tree_row_words(b->max_q_len);
+    a.tree_stride = tree_stride;
   }
   a.max_q_len = b->max_q_len;
   a.max_seq_len = b->max_seq_len;

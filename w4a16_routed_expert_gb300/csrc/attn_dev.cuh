@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "attn.h"
+#include "attn_tree.h"
 #include "common.cuh"
 
 namespace moe {
@@ -61,16 +62,10 @@ __device__ __forceinline__ int keys_seen(const AttnArgs& a, int keys, int n, int
   return a.causal ? min(keys, max(0, keys - n + i + 1)) : keys;
 }
 
-// 32 bits of a drafted token's row of AttnArgs::tree from bit `off` on, which
-// may lie before its first: those are keys of the context, all seen.
-__device__ __forceinline__ uint32_t tree_window(const uint32_t* row, int words, int off) {
-  if (off <= -32) return 0xffffffffu;
-  const int w = off >> 5;  // -1 or more
-  const uint32_t lo = w < 0 ? 0xffffffffu : w < words ? __ldg(row + w) : 0u;
-  const uint32_t hi = (off & 31) && w + 1 < words ? __ldg(row + w + 1) : 0u;
-  return __funnelshift_r(lo, hi, off & 31);
-}
-// The first n bits (all for 32 and more, none for 0 and less).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// A drafted token's row of AttnArgs::tree (tree_window).
+struct TreeRow {
+  const uint32_t* at;
+  __device__ __forceinline__ uint32_t operator[](int w) const { return __ldg(at + w); }
+};
 
 }  // namespace moe

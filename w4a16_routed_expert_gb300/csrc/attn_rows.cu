@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[m][e] = lr[m][e] = 0.f;
           const int row = s.row0 + min((wr * MT + m) * 16 + g8 + 8 * e, s.rows - 1);
           if (TREE)
-            lim[m][e] = (s.t0 + row / a.g) * a.tree_words;
+            lim[m][e] = (s.t0 + row / a.g) * a.tree_stride;
           else
             lim[m][e] = s.b < 0 ? s.klen : keys_seen(a, s.klen, s.n, row / a.g);
         }
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int w = 0; w < NV; ++w) {
                   vis[m][e][w] = low_bits(s.klen - k0 - w * 32);
                   if (s.b >= 0)
-                    vis[m][e][w] &= tree_window(a.tree + lim[m][e], a.tree_words, k0 + w * 32 - all_see);
+                    vis[m][e][w] &= tree_window(TreeRow{a.tree + lim[m][e]}, a.tree_words, k0 + w * 32 - all_see);
                 }
           }
         }

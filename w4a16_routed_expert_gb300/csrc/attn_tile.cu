@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
         const int all_see = cur->b < 0 ? cur->klen
                             : TREE     ? cur->klen - cur->n
                                        : keys_seen(a, cur->klen, cur->n, cur->row0 / a.g);
-        const uint32_t* bits = TREE && cur->b >= 0 ? a.tree + (long long)(cur->t0 + row / a.g) * a.tree_words : nullptr;
+        const uint32_t* bits = TREE && cur->b >= 0 ? a.tree + (long long)(cur->t0 + row / a.g) * a.tree_stride : nullptr;
         const int tile0 = cur->tile, front = cur->front, nkeys = cur->nkeys;
 #pragma unroll 1
         for (int i = dual ? t : 0; i < tiles; i += dual ? 2 : 1) {
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
             for (int c = 0; c < 4; ++c) vis[c] = low_bits(seen - k0 - c * 32);
             if (bits && !pre) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) vis[c] &= tree_window(bits, a.tree_words, k0 + c * 32 - all_see);
+              for (int c = 0; c < 4; ++c) vis[c] &= tree_window(TreeRow{bits}, a.tree_words, k0 + c * 32 - all_see);
             }
             sees = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
           }
