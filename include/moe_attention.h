@@ -261,7 +261,9 @@ moe_status_t moe_attn_accept(moe_attn_t* attn, const moe_attn_accept_t* accept, 
  * path[b][i] to key seq_lens[b] - m + i for i < counts[b], m the sequence's
  * tokens; in the caches of all n handles, which must be of one shape, type and
  * strides and no cache twice (one handle's keys and values may be one cache).
- *   path    device [num_seqs][path_stride], ascending from i or more
+ *   path    device [num_seqs][path_stride], ascending from i or more;
+ *           moe_attn_keep_strided: rows of path_len nodes, path_stride (at least
+ *           that) words apart; none behind a row's path_len is read
  *   counts  device [num_seqs]
  * Errors are recorded in attns[0]: a path or count out of order or range, a
  * page beyond the cache; what stands before it in the path is moved. */
@@ -269,6 +271,10 @@ moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs
                            const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
                            int32_t table_stride, const int32_t* path, int32_t path_stride, const int32_t* counts,
                            void* stream);
+moe_status_t moe_attn_keep_strided(moe_attn_t* const* attns, int32_t n, int32_t num_seqs, const int32_t* q_offsets,
+                                   const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
+                                   int32_t table_stride, const int32_t* path, int32_t path_stride, int32_t path_len,
+                                   const int32_t* counts, void* stream);
 
 /* Synchronises `stream` and reports (then clears) the first of what the
  * handle's kernels recorded, on this stream or on others, since the last report:

@@ -66,3 +66,47 @@ def test_a_tree_in_the_last_columns_of_a_wider_array(D, Hq, nodes, context):
     want = a.forward(q.cuda(), tree=bits, **args)
     assert torch.equal(a.forward(q.cuda(), tree=wide[:, 3:], **args), want)
     a.sync()
+
+
+def numbered(pages=8, page=16, heads=2, dim=64):
+    kc, vc = caches(pages, page, heads, dim, F16, "slot", fill=0.0)
+    kc.copy_(torch.arange(pages * page, device="cuda").view(pages, page, 1, 1).expand_as(kc))
+    vc.copy_(kc)
+    return PagedAttention(num_q_heads=heads, num_kv_heads=heads, head_dim=dim, max_seqs=2, k_cache=kc, v_cache=vc), kc, vc
+
+
+@pytest.mark.parametrize("width,lo", [(4, 0), (7, 3), (64, 60), (130, 126)])
+def test_keep_of_paths_in_columns_of_a_wider_array(width, lo):
+    """Two sequences' paths of four nodes: the words beside them are no nodes, and
+    a count that passes the four is out of range."""
+    table, off, lens = ints([[1, 4], [3, 6]]), ints([0, 9, 18]), ints([20, 25])
+    paths, counts = [[0, 2, 3, 8], [0, 4, 5, 7]], [4, 3]
+    a, kc, vc = numbered()
+    place = lambda b, key: table[b, key // 16].item() * 16 + key % 16  # noqa: E731
+    want = list(range(8 * 16))
+    for b, start in enumerate((11, 16)):
+        for i in range(counts[b]):
+            want[place(b, start + i)] = place(b, start + paths[b][i])
+    wide = torch.arange(width, dtype=torch.int32, device="cuda").repeat(2, 1)  # (ascending: would pass for nodes)
+    wide[:, lo:lo + 4] = ints(paths)
+    args = dict(q_offsets=off, seq_lens=lens, max_seq_len=32, block_table=table)
+    a.keep(wide[:, lo:lo + 4], ints(counts), **args)
+    a.sync()
+    assert kc[:, :, 1, 5].flatten().tolist() == want and torch.equal(kc, vc)
+    a, kc, vc = numbered()
+    a.keep(wide[:, lo:lo + 4], ints([5, 3]), **args)
+    with pytest.raises(capi.MoEError) as e:
+        a.sync()
+    assert e.value.status == capi.MOE_ERR_INVALID_ARG
+    got = kc[:, :, 1, 5].flatten().tolist()
+    assert [got[place(0, k)] for k in range(20)] == [place(0, k) for k in range(20)]  # its sequence is left alone
+    assert [got[place(1, 16 + i)] for i in range(3)] == [place(1, 16 + n) for n in (0, 4, 5)]
+
+
+def test_keep_strided_refuses_rows_that_overlap():
+    a, kc, _ = numbered()
+    x = torch.zeros(64, dtype=torch.int32, device="cuda").data_ptr()
+    one = (ctypes.c_void_p * 1)(a.handle)
+    for stride, width in ((3, 4), (4, 0), (0, 0), (4, -1)):
+        assert capi.lib().moe_attn_keep_strided(one, 1, 2, x, x, 16, x, 1, x, stride, width, x, None) == capi.MOE_ERR_INVALID_ARG
+    assert capi.lib().moe_attn_keep_strided(one, 1, 0, x, x, 16, x, 1, x, 4, 3, x, None) == capi.MOE_OK

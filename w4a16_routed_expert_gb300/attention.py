@@ -374,12 +374,13 @@ class PagedAttention:
                 raise ValueError(f"{name}: cuda int32 [{B}][1 or more]")
         if max_seq_len > block_table.shape[1] * self.cfg.page_size:
             raise ValueError("max_seq_len is beyond the block table")
-        n = 1 + len(others)
-        st = self._lib.moe_attn_keep(
-            (capi._P * n)(self.handle, *[a.handle for a in others]), n, B, self._ints("q_offsets", q_offsets, B + 1),
-            self._ints("seq_lens", seq_lens, B), max_seq_len, block_table.data_ptr(),
-            block_table.stride(0) if B > 1 else block_table.shape[1], path.data_ptr(),
-            path.stride(0) if B > 1 else path.shape[1], self._ints("counts", counts, B), self._stream(stream, counts))
+        n, width, stride = 1 + len(others), path.shape[1], path.stride(0) if B > 1 else path.shape[1]
+        args = ((capi._P * n)(self.handle, *[a.handle for a in others]), n, B, self._ints("q_offsets", q_offsets, B + 1),
+                self._ints("seq_lens", seq_lens, B), max_seq_len, block_table.data_ptr(),
+                block_table.stride(0) if B > 1 else block_table.shape[1], path.data_ptr(), stride)
+        counts, on = self._ints("counts", counts, B), self._stream(stream, counts)
+        st = (self._lib.moe_attn_keep(*args, counts, on) if stride == width
+              else self._lib.moe_attn_keep_strided(*args, width, counts, on))
         if st:
             capi.check(st, "moe_attn_keep")
 

@@ -142,6 +142,7 @@ PROTOTYPES = {
     "moe_attn_plan": (_I32, [_P, ctypes.POINTER(moe_attn_plan_t), _P]),
     "moe_attn_accept": (_I32, [_P, ctypes.POINTER(moe_attn_accept_t), _P]),
     "moe_attn_keep": (_I32, [ctypes.POINTER(_P), _I32, _I32, _P, _P, _I32, _P, _I32, _P, _I32, _P, _P]),
+    "moe_attn_keep_strided": (_I32, [ctypes.POINTER(_P), _I32, _I32, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _P, _P]),
     "moe_attn_sync": (_I32, [_P, _P]),
     "moe_attn_destroy": (_I32, [_P]),
     # include/moe_residency.h

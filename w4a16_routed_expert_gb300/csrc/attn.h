@@ -207,7 +207,8 @@ cudaError_t launch_attn_accept(const AcceptArgs& a, cudaStream_t s, bool pdl);
 constexpr int kKeepCaches = 64;
 struct KeepArgs {
   void* caches[kKeepCaches];
-  int count, B, Hk, D, page_size, num_pages, max_seq_len, table_stride, path_stride;
+  int count, B, Hk, D, page_size, num_pages, max_seq_len, table_stride;
+  int path_stride, path_len;  // from one sequence's path to the next, its words
   long long page_stride, slot_stride, head_stride;
   const int32_t *q_offsets, *seq_lens, *block_table, *path, *counts;
   uint32_t* err;

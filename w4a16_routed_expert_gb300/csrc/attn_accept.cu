@@ -108,14 +108,14 @@ __global__ void __launch_bounds__(kKeepThreads) k_attn_keep(const __grid_constan
   const int32_t* path = a.path + (long long)b * a.path_stride;
   int p = -1, before = -1;
   auto ask = [&](int j) {
-    if (tid < kKeepPath && j < a.path_stride) {
+    if (tid < kKeepPath && j < a.path_len) {
       p = __ldg(path + j);
       before = j ? __ldg(path + j - 1) : -1;
     }
   };
   ask(tid);
   const int m = max(hi - lo, 0), start = len - m;
-  const bool bad = hi < lo || len < 0 || len > a.max_seq_len || count < 0 || count > min(m, a.path_stride) ||
+  const bool bad = hi < lo || len < 0 || len > a.max_seq_len || count < 0 || count > min(m, a.path_len) ||
                    (count > 0 && start < 0);
   if (bad) {
     if (tid == 0) record_error(a.err, kAttnErrBounds);

@@ -425,6 +425,67 @@ moe_status_t forward_call(moe_attn* h, const char* fn, const void* q, int64_t q_
   return forward(h, fn, a, static_cast<cudaStream_t>(stream));
 }
 
+// A keep of the caller's arguments: paths of path_len nodes, path_stride words apart.
+moe_status_t keep_call(const char* fn, moe_attn_t* const* attns, int32_t n, int32_t num_seqs, const int32_t* q_offsets,
+                       const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table, int32_t table_stride,
+                       const int32_t* path, int32_t path_stride, int32_t path_len, const int32_t* counts, void* stream) {
+  if (!attns || n < 1 || n > 1024) return set_error(MOE_ERR_INVALID_ARG, "%s: 1 to 1024 handles, got %d", fn, n);
+  const void* caches[2 * 1024];
+  int count = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_attn* h = attns[i];
+    const moe_status_t st = check_handle(h, fn);
+    if (st != MOE_OK) return st;
+    if (!h->buf.k_cache) return set_error(MOE_ERR_INVALID_ARG, "%s: handle %d has no cache", fn, i);
+    const moe_attn_config_t &c = h->cfg, &f = attns[0]->cfg;
+    if (c.num_kv_heads != f.num_kv_heads || c.head_dim != f.head_dim || c.dtype != f.dtype ||
+        c.page_size != f.page_size || c.num_pages != f.num_pages || c.page_stride != f.page_stride ||
+        c.slot_stride != f.slot_stride || c.head_stride != f.head_stride)
+      return set_error(MOE_ERR_INVALID_ARG, "%s: the cache of handle %d has another shape, type or strides", fn, i);
+    caches[count++] = h->buf.k_cache;
+    if (h->buf.v_cache != h->buf.k_cache) caches[count++] = h->buf.v_cache;
+  }
+  std::sort(caches, caches + count, std::less<const void*>());
+  if (std::adjacent_find(caches, caches + count) != caches + count)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: the same cache twice", fn);
+  const moe_attn* h = attns[0];
+  if (num_seqs < 0 || num_seqs > 4096)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..4096", fn, num_seqs);
+  if (num_seqs == 0) return MOE_OK;
+  if (!q_offsets || !seq_lens || !block_table || !path || !counts)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: arrays must not be NULL", fn);
+  if (table_stride < 1 || path_len < 1 || path_stride < path_len || max_seq_len < 0)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: table_stride and path's row must be positive, max_seq_len not negative", fn);
+  if ((long long)max_seq_len > (long long)table_stride * h->cfg.page_size)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len=%d beyond table_stride * page_size", fn, max_seq_len);
+  moe::KeepArgs a = {};
+  a.B = num_seqs;
+  a.Hk = h->cfg.num_kv_heads;
+  a.D = h->cfg.head_dim;
+  a.page_size = h->cfg.page_size;
+  a.num_pages = (int)h->cfg.num_pages;
+  a.max_seq_len = max_seq_len;
+  a.table_stride = table_stride;
+  a.path_stride = path_stride;
+  a.path_len = path_len;
+  a.page_stride = h->cfg.page_stride;
+  a.slot_stride = h->cfg.slot_stride;
+  a.head_stride = h->cfg.head_stride;
+  a.q_offsets = q_offsets;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.path = path;
+  a.counts = counts;
+  a.err = h->err;
+  for (int i = 0; i < count; i += moe::kKeepCaches) {
+    a.count = std::min(count - i, moe::kKeepCaches);
+    for (int k = 0; k < a.count; ++k) a.caches[k] = const_cast<void*>(caches[i + k]);
+    const cudaError_t e = moe::launch_attn_keep(a, h->num_sms, static_cast<cudaStream_t>(stream), h->pdl);
+    if (e != cudaSuccess) return cuda_error(e, fn);
+  }
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -713,62 +774,16 @@ moe_status_t moe_attn_keep(moe_attn_t* const* attns, int32_t n, int32_t num_seqs
                            const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
                            int32_t table_stride, const int32_t* path, int32_t path_stride, const int32_t* counts,
                            void* stream) {
-  const char* fn = "moe_attn_keep";
-  if (!attns || n < 1 || n > 1024) return set_error(MOE_ERR_INVALID_ARG, "%s: 1 to 1024 handles, got %d", fn, n);
-  const void* caches[2 * 1024];
-  int count = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    const moe_attn* h = attns[i];
-    const moe_status_t st = check_handle(h, fn);
-    if (st != MOE_OK) return st;
-    if (!h->buf.k_cache) return set_error(MOE_ERR_INVALID_ARG, "%s: handle %d has no cache", fn, i);
-    const moe_attn_config_t &c = h->cfg, &f = attns[0]->cfg;
-    if (c.num_kv_heads != f.num_kv_heads || c.head_dim != f.head_dim || c.dtype != f.dtype ||
-        c.page_size != f.page_size || c.num_pages != f.num_pages || c.page_stride != f.page_stride ||
-        c.slot_stride != f.slot_stride || c.head_stride != f.head_stride)
-      return set_error(MOE_ERR_INVALID_ARG, "%s: the cache of handle %d has another shape, type or strides", fn, i);
-    caches[count++] = h->buf.k_cache;
-    if (h->buf.v_cache != h->buf.k_cache) caches[count++] = h->buf.v_cache;
-  }
-  std::sort(caches, caches + count, std::less<const void*>());
-  if (std::adjacent_find(caches, caches + count) != caches + count)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: the same cache twice", fn);
-  const moe_attn* h = attns[0];
-  if (num_seqs < 0 || num_seqs > 4096)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: num_seqs=%d out of 0..4096", fn, num_seqs);
-  if (num_seqs == 0) return MOE_OK;
-  if (!q_offsets || !seq_lens || !block_table || !path || !counts)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: arrays must not be NULL", fn);
-  if (table_stride < 1 || path_stride < 1 || max_seq_len < 0)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: table_stride and path_stride must be positive, max_seq_len not negative",
-                     fn);
-  if ((long long)max_seq_len > (long long)table_stride * h->cfg.page_size)
-    return set_error(MOE_ERR_INVALID_ARG, "%s: max_seq_len=%d beyond table_stride * page_size", fn, max_seq_len);
-  moe::KeepArgs a = {};
-  a.B = num_seqs;
-  a.Hk = h->cfg.num_kv_heads;
-  a.D = h->cfg.head_dim;
-  a.page_size = h->cfg.page_size;
-  a.num_pages = (int)h->cfg.num_pages;
-  a.max_seq_len = max_seq_len;
-  a.table_stride = table_stride;
-  a.path_stride = path_stride;
-  a.page_stride = h->cfg.page_stride;
-  a.slot_stride = h->cfg.slot_stride;
-  a.head_stride = h->cfg.head_stride;
-  a.q_offsets = q_offsets;
-  a.seq_lens = seq_lens;
-  a.block_table = block_table;
-  a.path = path;
-  a.counts = counts;
-  a.err = h->err;
-  for (int i = 0; i < count; i += moe::kKeepCaches) {
-    a.count = std::min(count - i, moe::kKeepCaches);
-    for (int k = 0; k < a.count; ++k) a.caches[k] = const_cast<void*>(caches[i + k]);
-    const cudaError_t e = moe::launch_attn_keep(a, h->num_sms, static_cast<cudaStream_t>(stream), h->pdl);
-    if (e != cudaSuccess) return cuda_error(e, fn);
-  }
-  return MOE_OK;
+  return keep_call("moe_attn_keep", attns, n, num_seqs, q_offsets, seq_lens, max_seq_len, block_table, table_stride, path,
+                   path_stride, path_stride, counts, stream);
+}
+
+moe_status_t moe_attn_keep_strided(moe_attn_t* const* attns, int32_t n, int32_t num_seqs, const int32_t* q_offsets,
+                                   const int32_t* seq_lens, int32_t max_seq_len, const int32_t* block_table,
+                                   int32_t table_stride, const int32_t* path, int32_t path_stride, int32_t path_len,
+                                   const int32_t* counts, void* stream) {
+  return keep_call("moe_attn_keep_strided", attns, n, num_seqs, q_offsets, seq_lens, max_seq_len, block_table,
+                   table_stride, path, path_stride, path_len, counts, stream);
 }
 
 moe_status_t moe_attn_sync(moe_attn_t* h, void* stream) {
