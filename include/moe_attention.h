@@ -224,7 +224,9 @@ typedef struct {
 
 /* Fills a step's tables. Tokens behind the last sequence get position 0, slot
  * -1 and no bits; ring places and table entries that the step does not give out
- * or take back stay as they were. One plan at a time per handle. A length,
+ * or take back stay as they were. One plan at a time per handle. Lengths that
+ * stand in an output (the last step's seq_lens as context_lens, in the same
+ * tables) are refused: MOE_ERR_INVALID_ARG. A length,
  * parent, page or count out of range (a context that is negative, a sequence
  * longer than its row of the table or 2^30, more tokens than T or max_nodes, a parent
  * not before its child, a free page beyond the cache) is recorded (moe_attn_sync:

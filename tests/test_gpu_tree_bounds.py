@@ -14,7 +14,7 @@ import numpy as np  # noqa: E402
 import tree_oracle as TO  # noqa: E402
 from test_gpu_attention import F16, _cuda, build, caches  # noqa: E402,F401
 from w4a16_routed_expert_gb300 import capi  # noqa: E402
-from w4a16_routed_expert_gb300.attention import PagedAttention  # noqa: E402
+from w4a16_routed_expert_gb300.attention import PagedAttention, PagePool, StepTables  # noqa: E402
 
 
 def ints(x):
@@ -110,3 +110,27 @@ def test_keep_strided_refuses_rows_that_overlap():
     for stride, width in ((3, 4), (4, 0), (0, 0), (4, -1)):
         assert capi.lib().moe_attn_keep_strided(one, 1, 2, x, x, 16, x, 1, x, stride, width, x, None) == capi.MOE_ERR_INVALID_ARG
     assert capi.lib().moe_attn_keep_strided(one, 1, 0, x, x, 16, x, 1, x, 4, 3, x, None) == capi.MOE_OK
+
+
+def test_plan_refuses_its_own_lengths():
+    """The last step's seq_lens as lengths: refused in the same tables, right in
+    others and as a copy."""
+    kc, vc = caches(8, 16, 1, 8, F16, "slot", fill=0.0)
+    a = PagedAttention(num_q_heads=1, num_kv_heads=1, head_dim=8, k_cache=kc, v_cache=vc)
+    pool = PagePool.of(torch.arange(8, dtype=torch.int32, device="cuda"), num_seqs=2, max_pages=4)
+    t, u = (StepTables(num_seqs=2, num_tokens=20) for _ in range(2))
+    new = ints([13, 2])
+    a.plan(pool, ints([0, 0]), new, t)
+    was = [x.clone() for x in (pool.state, t.seq_lens, t.slots)]
+    for lengths in ((t.seq_lens, new), (new, t.seq_lens), (t.q_offsets[:2], new), (t.slots[18:], new)):
+        with pytest.raises(capi.MoEError) as e:
+            a.plan(pool, *lengths, t)
+        assert e.value.status == capi.MOE_ERR_INVALID_ARG
+    assert all(torch.equal(x, y) for x, y in zip(was, (pool.state, t.seq_lens, t.slots)))
+    held = pool.state.clone()
+    a.plan(pool, t.seq_lens, new, u, next_state=torch.empty_like(held))
+    want = [x.clone() for x in (u.q_offsets, u.seq_lens, u.positions, u.slots)]
+    a.plan(pool, t.seq_lens.clone(), new, t)
+    a.sync()
+    assert all(torch.equal(x, y) for x, y in zip(want, (t.q_offsets, t.seq_lens, t.positions, t.slots)))
+    assert t.seq_lens.tolist() == [26, 4] and t.positions[:15].tolist() == list(range(13, 26)) + [2, 3]

@@ -303,7 +303,8 @@ class PagedAttention:
         returns them.
 
         Sequence b holds context_lens[b] own keys and adds new_lens[b] tokens
-        (-1: it ends and gives its pages back); the pages that they need come
+        (-1: it ends and gives its pages back; neither may stand in the tables
+        themselves, as their seq_lens do: copy those); the pages that they need come
         from the pool in order of sequences, and one whose need it cannot meet
         (nor any later one that needs some) gets seq_lens 0 and slots -1.
         parents (tables with max_nodes): int32, of each new token the new token

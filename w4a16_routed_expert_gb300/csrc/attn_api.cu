@@ -10,6 +10,7 @@
 #include <new>
 
 #include "attn.h"
+#include "attn_plan.h"
 #include "attn_tree.h"
 #include "layer_internal.h"
 #include "moe_attention.h"
@@ -706,6 +707,8 @@ moe_status_t moe_attn_plan(moe_attn_t* h, const moe_attn_plan_t* p, void* stream
     return set_error(MOE_ERR_INVALID_ARG, "%s: context_lens, new_lens, block_table and seq_lens must not be NULL", fn);
   if (p->num_tokens > 0 && (!p->positions || !p->slots || (p->max_nodes > 0 && (!p->parents || !p->tree))))
     return set_error(MOE_ERR_INVALID_ARG, "%s: positions, slots and, with trees, parents and tree must not be NULL", fn);
+  if (moe::plan_overlaps_lengths(*p))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: context_lens and new_lens must not stand in an output (seq_lens, say)", fn);
   moe::PlanArgs a = {};
   a.B = p->num_seqs;
   a.T = p->num_tokens;

@@ -1,6 +1,8 @@
-// The arithmetic of a step's running sums (attn_plan.cu), in plain C++ so that
-// it can be checked without a GPU.
+// The arithmetic of a step's running sums (attn_plan.cu) and a check of its
+// arguments, in plain C++ so that they can be run without a GPU.
 #pragma once
+
+#include <cstdint>
 
 #ifdef __CUDACC__
 #define MOE_PLAN_FN __host__ __device__ __forceinline__
@@ -43,6 +45,24 @@ MOE_PLAN_FN PlanAsk plan_ask(int T, int max_nodes, int table_stride, int page_si
   }
   k.back = k.valid && fresh < 0 ? held : 0;
   return k;
+}
+
+// Whether the lengths stand in an output: every block reads them more than once,
+// when others have stored theirs already. Plan: moe_attn_plan_t.
+template <typename Plan>
+inline bool plan_overlaps_lengths(const Plan& p) {
+  const long long B = p.num_seqs, T = p.num_tokens, words = (p.max_nodes + 31) / 32;
+  const struct {
+    const void* at;
+    long long n;
+  } out[] = {{p.q_offsets, B + 1}, {p.seq_lens, B}, {p.positions, T}, {p.slots, T}, {p.tree, T * words}, {p.state_out, B + 2}};
+  const int32_t* const in[] = {p.context_lens, p.new_lens};
+  for (const int32_t* lengths : in)
+    for (const auto& o : out) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(lengths), y = reinterpret_cast<uintptr_t>(o.at);
+      if (lengths && o.at && o.n > 0 && x < y + (uintptr_t)o.n * 4 && y < x + (uintptr_t)B * 4) return true;
+    }
+  return false;
 }
 
 }  // namespace moe
