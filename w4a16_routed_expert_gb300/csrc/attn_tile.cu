@@ -91,7 +91,8 @@ struct Misc {
   uint32_t tmem;
   int abort_flag;
   int mma_issued;
-  int32_t phase[kMaxStages];  // of the stage's last copy, -1: none
+  int issued;                 // stages handed to TMA by one warp
+  int32_t phase[kMaxStages];  // kTwoCopy: of the stage's last copy, -1: none
   int32_t scratch[kThreadsOf<true, 128> / 32];
 };
 static_assert(sizeof(Misc) <= 96, "SmemPlan's room for Misc");
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
 
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
-      misc->phase[i] = -1;
+      if (kTwo) misc->phase[i] = -1;
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
     mbar_init(ml_full, 8);
     mbar_init(o_read, 4);
     misc->abort_flag = 0;
+    misc->issued = 0;
     misc->mma_issued = 0;
     fence_mbar_init();
   }
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
     const bool split = (a.D & 63) != 0;
     const int cx = split ? hf * 64 : 0, ch = split ? 0 : hf;
     const uint32_t dst0 = smem_u32(smem) + sp.ring + (uint32_t)hf * kHalf + (uint32_t)c * box * 128;
-    int st = 0, slot_i = 0;
+    int st = 0, issued = 0, slot_i = 0;
     uint32_t ph = 0, sph = 0;
     bool ok = true;
     Walk<kKT, kTileRows> w;
@@ -263,16 +265,22 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
         z = y;
       };
       auto issue = [&](const CUtensorMap* tm, int y, bool some_keys, int page, int at, int boxes) {
-        to(y);
+        if (kTwo) to(y);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.err));
         if (!ok) return;
         if (lane == 0) {
-          misc->phase[st] = (int)ph;
+          if (kTwo) misc->phase[st] = (int)ph;
           mbar_arrive_expect_tx(&full[st], (uint32_t)boxes * box * 128 * NH);
         }
         __syncwarp();
         if (some_keys)
           tma_load_5d(dst0 + (uint32_t)st * kTileBytes, tm, cx, at, ch, s.h, page_in_cache(a, page), &full[st]);
+        if (kTwo) return;
+        ++issued;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+        }
       };
       int page = page_of(s.tile);
       // (the first page's number is on its way meanwhile)
@@ -323,8 +331,9 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
           page = next;
         }
       }
-      to(2 * s.tiles);
+      if (kTwo) to(2 * s.tiles);
     }
+    if (!kTwo && lane == 0) misc->issued = issued;
   } else if (warp == kWarpMma) {
     // ----------------------------------------------------------------- MMA
     {
@@ -621,8 +630,16 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
         more = peek_segment();
         const Segment* n = &segs[slot_i];
         more_q = more && (t == 0 || n->rows > 128);
-        if (more && (dual ? last : t == 0)) load_q(n, 0);
-        if (more_q && t == 1) load_q(n, 1);
+        // (Heads to 64 that are not over trees: one copy of the loop for both row
+        // tiles, and `first` below found again where it is used; with either as in
+        // the other kernels theirs spills, 48 sequences of drafts 50.0 us, so 48.3.
+        // Heads above 64 are faster with two: chunks 355, 361 with one.)
+        if (!TREE && DP == 64) {
+          if (more_q) load_q(n, t);
+        } else {
+          if (more && (dual ? last : t == 0)) load_q(n, 0);
+          if (more_q && t == 1) load_q(n, 1);
+        }
       };
       float mref = -INFINITY;
       // sums of the weights, and (RSUM) of the weights as rounded: the quotient
@@ -690,7 +707,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
                   if (k0 + c * 32 + e >= seen) v[e] = 0xff800000u;
               }
             };
-            bool move = first;
+            bool move = TREE ? first : i == 0;
 #pragma unroll 1
             while (true) {  // a pass that moves the reference is the last
               if (move) {
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
                 l2.y *= f;
                 lr2.x *= f;
                 lr2.y *= f;
-                if (!first) {
+                if (TREE ? !first : i > 0) {
                   if (kAhead && !dual) {  // the P V before has been issued, but need not be over
                     const int j = i - 1;
                     mbar_wait(&o_full[2 * t + (j & 1)], (outs[j & 1] + (uint32_t)(j >> 1)) & 1u, abort_flag, a.err);
@@ -944,8 +961,11 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
   if (misc->abort_flag) {
     // a block that gave up lets its copies and MMAs end before it leaves
     if (warp == kWarpCopy && lane == 0) {
-      for (int i = 0; i < stages; ++i)
-        if (misc->phase[i] >= 0) mbar_wait(&full[i], (uint32_t)misc->phase[i], nullptr, nullptr);
+      const int n = misc->issued;
+      for (int i = 0; i < stages; ++i) {
+        const int phase = kTwo ? misc->phase[i] : i < n ? (n - 1 - i) / stages & 1 : -1;
+        if (phase >= 0) mbar_wait(&full[i], (uint32_t)phase, nullptr, nullptr);
+      }
     }
     if (warp == kWarpMma && misc->mma_issued) {
       commit_elect(elect_one(), drain);  // the lane that issued the MMAs
