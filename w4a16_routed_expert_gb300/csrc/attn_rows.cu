@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return (uint32_t)(key >> box_log2) * box * DP * 2 + (uint32_t)(key & (box - 1)) * 128;
     };
     const uint32_t half_step = (uint32_t)box * 128;
+    const uint32_t warp_off = keys_off(warp * 16);  // WR 1: a warp's keys stand in one place of every stage
     const int krow = (lane & 7) + ((lane >> 4) << 3), ksel = (lane >> 3) & 1;
     const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vsel = lane >> 4;
     const uint32_t qs = smem_u32(smem + sp.q);
@@ -255,13 +256,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < kQ; ++i) {
         const int z = tid + i * kWarps * 32, r = z / (DP / 8), c8 = z % (DP / 8);
         const bool valid = r < s.rows && c8 * 8 < a.D;
-        const int row = s.row0 + r, tok = row / a.g, hq = s.h * a.g + row - tok * a.g;
-        const T* src = static_cast<const T*>(a.q) + (long long)(s.t0 + tok) * a.q_stride + (long long)hq * a.D + c8 * 8;
+        auto word = [&]() {  // (its divisions are for words that there are: a group of one to three rows has few)
+          const int row = s.row0 + r, tok = row / a.g, hq = s.h * a.g + row - tok * a.g;
+          return static_cast<const T*>(a.q) + (long long)(s.t0 + tok) * a.q_stride + (long long)hq * a.D + c8 * 8;
+        };
         if (kAsyncQ) {
+          const T* src = word();
           cp_async16(smem_u32(smem) + q_place(r, c8), valid ? (const void*)src : a.q, valid);
         } else {
           qv[kAsyncQ ? 0 : i] = make_uint4(0, 0, 0, 0);
-          if (valid) qv[kAsyncQ ? 0 : i] = *reinterpret_cast<const uint4*>(src);
+          if (valid) qv[kAsyncQ ? 0 : i] = *reinterpret_cast<const uint4*>(word());
         }
       }
     };
@@ -339,13 +343,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t stage = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes;
           uint32_t kb[KS];  // each sixteen keys (all in one box); the values kTileBytes behind them
 #pragma unroll
-          for (int j = 0; j < KS; ++j) kb[j] = stage + keys_off(key + 16 * j);
+          for (int j = 0; j < KS; ++j) kb[j] = stage + (WR == 1 ? warp_off : keys_off(key + 16 * j));
           if (here < 16 * KS) {
             // slots past the end may hold anything: their values become zeros
             // (a zero weight would not stop a NaN); their logits are masked
             for (int z = lane; z < (16 * KS - here) * (DP / 8); z += 32) {
               const int r = here + z / (DP / 8), c8 = z % (DP / 8);
-              *reinterpret_cast<uint4*>(smem + (stage + kTileBytes - smem_u32(smem)) + keys_off(key + r) +
+              *reinterpret_cast<uint4*>(smem + (stage + kTileBytes - smem_u32(smem)) +
+                                        (WR == 1 ? warp_off + (uint32_t)r * 128 : keys_off(key + r)) +
                                         (uint32_t)(c8 >> 3) * half_step + (uint32_t)((c8 & 7) << 4)) =
                   make_uint4(0, 0, 0, 0);
             }
