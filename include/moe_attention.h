@@ -22,7 +22,10 @@
  *            rows of all tokens: 256 of them, or 16 (32 at head sizes to 64)
  *            where few rows read a key; where the batch has as many tokens as
  *            fill a block of 256 rows for each sequence on average, once for
- *            every block of each sequence's rows, together with its own keys
+ *            every block of each sequence's rows, together with its own keys.
+ *            (Over trees the few rows' blocks are of 16, 32 or 64, and where
+ *            lengths are short the prefix may be read for every 128 or 256 rows
+ *            of each sequence, however few tokens there are)
  *
  * and, around a step that checks trees of drafted tokens (the lengths then
  * stand on the GPU, where it is first known how many were right):
@@ -43,7 +46,8 @@
  * are rounded once when they are stored. (The probabilities that multiply
  * the values go to the tensor cores in the 16-bit type: in two parts, which
  * lose nothing beside the result's own rounding, where few rows read a key,
- * in one otherwise, and over trees from 17 rows on.)
+ * in one otherwise, and over trees from 17 rows on: a line of 17 to 32 rows of
+ * at most 64 elements is then a little less exact as a tree than as causal.)
  *
  * Conventions are those of moe_layer.h: every call returns a moe_status_t
  * (moe_layer_last_error(NULL) describes the calling thread's last failure),
@@ -180,9 +184,9 @@ moe_status_t moe_attn_forward(moe_attn_t* attn, const void* q, int64_t q_stride,
  * m of which are its m query tokens', token i sees the first n - m and key
  * n - m + j where bit j % 32 of tree[token * tree_stride + j / 32] is set; a
  * row with no bit sees not even itself. Bits from m on are ignored. The prefix
- * is seen by all; batch->causal is not looked at. A step may be padded: tokens
- * behind the last sequence's change nothing in the others' rows; their own get
- * zeros, or behind a prefix nothing of use.
+ * is seen by all; batch->causal is not looked at. A step may be padded (up to
+ * max_q_len * num_seqs tokens): tokens behind the last sequence's change nothing
+ * in the others' rows; their own get zeros, or behind a prefix nothing of use.
  *   tree         device [T], rows of W = max_q_len / 32 rounded up words; none
  *                behind a row's first W is read
  *   tree_stride  words from one token's row to the next, at least W;

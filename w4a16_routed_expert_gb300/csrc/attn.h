@@ -145,6 +145,8 @@ constexpr int kRowsKeyTile = 64;
 // of 128, trees of 16 tokens after up to 100, 250, 490 keys, whole / in a line:
 // one 7.6 / 8.5, 9.7 / 9.5, 12.0 / 10.4 us, 16 8.3 / 12.9, 10.6 / 15.4, 16.7 /
 // 19.6, 64 25.4 / 30.1, 32.4 / 35.8, 44.8 / 47.2; and the call's second launch.
+// (One bound for all: a lone sequence in a captured step, which pays for no
+// launch, would be better off in a line from about 240 keys on, many from 500.)
 constexpr int kWholeKeys = 320;
 struct AttnRowsPlan {
   int n_cta, stages, row_groups;

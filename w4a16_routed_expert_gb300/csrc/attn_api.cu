@@ -204,6 +204,7 @@ void fill_rope(const moe_attn* h, moe::RopeArgs* a) {
 //   64 rows, few-row kernel, groups 16, 128, 256: 1000 keys 14 / 15, 19 / 29,
 //   34 / 48, 3000 28 / 21, 39 / 55, 74 / 98; whole groups of both, 300 keys: 10 /
 //   14, 12 / 16, 22 / 19. Of 32 rows it is within 15% either way.
+// Between these sizes the estimate has not been held to measurements.
 int whole_rows(const moe::AttnArgs& a, int own_rows, int prefix_rows, bool tile, int num_sms) {
   if (own_rows <= 32 || (!tile && prefix_rows)) return 0;
   const double rows = (double)a.T * a.g;

@@ -1,13 +1,15 @@
 // Attention for few query rows to a key: a decode step over each sequence's
 // own pages, drafted tokens, or a prefix shared by a handful of rows.
 //
-// A group's rows (at most 16, or 32 in two tiles at head sizes to 64) meet a
-// run of its keys: S = Q K^T, running softmax, O += P V, one pass over the
-// keys. Every key and value is read once by one block, so the bound is
-// memory; what has to hold is that the SM's copies never wait. Per SM at the
-// measured copy rate a 16-key step (8 KB at head size 128) takes ~350 cycles;
-// its 16-row tiles cost ~150 issue slots, spread over the SM's eight computing
-// warps. That leaves room to multiply the probabilities in two 16-bit parts.
+// A group's rows (at most 16, or 32 in two tiles at head sizes to 64; over trees
+// 16, 32 or 64) meet a run of its keys: S = Q K^T, running softmax, O += P V, one
+// pass over the keys. Every key and value is read once by one block, so up to 16
+// rows the bound is memory; what has to hold is that the SM's copies never wait.
+// Per SM at the measured copy rate a 16-key step (8 KB at head size 128) takes
+// ~350 cycles; a 16-row tile costs ~150 issue slots, spread over the SM's eight
+// computing warps. That leaves room to multiply the probabilities in two 16-bit
+// parts; over trees of 17 rows and more it does not, there is one part, and the
+// products bind.
 // Measured: 32 sequences of up to 24000 own keys, 8 key heads of 128 (1.53
 // GB), 228 us = 6.7 TB/s, 0.99 of the measured copy rate; 16 behind 4099
 // shared keys with up to 1000 own (92 MB) 25 us: 4 us until the first copy
@@ -20,9 +22,12 @@
 //
 // A block is four computing warps and one that copies. Keys and values come
 // page by page as TMA boxes (16 to 64 slots of one head, 128-byte swizzle)
-// into a ring of 64-key stages; warp w takes keys 16w .. 16w+15 of each with
-// its own running maximum, sum and output tile in registers, and the four are
-// joined at the end of the block's part of a group. Two blocks per SM.
+// into a ring of 64-key stages. Where a group is one block of rows (WR 1) warp w
+// takes keys 16w .. 16w+15 of each with its own running maximum, sum and output
+// tile in registers, and the four are joined at the end of the block's part of a
+// group. Over trees of 17 to 32 rows two warps share each half of the rows, 32
+// keys of a stage each, and are joined in pairs; with 33 to 64 rows every warp
+// has 16 rows and all keys, and nothing is joined. Two blocks per SM.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -72,9 +77,9 @@ __device__ __forceinline__ bool bar_any(bool v) {
 }
 
 // WR: the computing warps are WR row groups of 16 MT rows by 4 / WR key groups;
-// a row group's warps share the 64 keys of a stage, 16 at a time. TREE: a token sees of its sequence's new tokens those that its bits name
-// (AttnArgs::tree); a tile that reaches behind the context takes a word of
-// them a row.
+// a row group's warps share the 64 keys of a stage. TREE: a token sees of its
+// sequence's new tokens those that its bits name (AttnArgs::tree); a tile that
+// reaches behind the context takes a word of them a row.
 template <typename T, int DP, int MT, int WR, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
     k_attn_rows(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a,

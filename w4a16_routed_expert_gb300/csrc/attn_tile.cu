@@ -11,7 +11,7 @@
 // measured copy rate): up to ~190 rows the keys' bytes bound it, above that
 // the products.
 // Measured: four chunks of 301 to 1024 tokens behind 8200 keys, 32 query and 8
-// key heads of 128, 370 us = 1.30 PFLOP/s, 0.67 of the measured bf16 rate; a
+// key heads of 128, 357 us = 1.35 PFLOP/s, 0.70 of the measured bf16 rate; a
 // key tile took 2700 to 2950 cycles when that was 361 us. P V runs at the tensor cores' rate
 // (64 cycles an MMA), Q K^T, which reads both operands from shared memory, at
 // ~95; the softmax of a row tile takes 1000 to 1300 and hides.
@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kThreadsOf<TREE, DP>, 1)
         more_q = more && (t == 0 || n->rows > 128);
         // (Heads to 64 that are not over trees: one copy of the loop for both row
         // tiles, and `first` below found again where it is used; with either as in
-        // the other kernels theirs spills, 48 sequences of drafts 50.0 us, so 48.3.
-        // Heads above 64 are faster with two: chunks 355, 361 with one.)
+        // the other kernels theirs spills, and 48 sequences of drafts take 1.7 us
+        // longer. Heads above 64 are faster with two: chunks 355 us, 361 with one.)
         if (!TREE && DP == 64) {
           if (more_q) load_q(n, t);
         } else {
