@@ -46,6 +46,7 @@ def test_apart(overlap):
     assert not overlap(num_tokens=0, max_nodes=0, positions=None, slots=None, tree=None, parents=None)
     assert not overlap(num_seqs=0, context_lens=None, new_lens=None, seq_lens=None)
     assert not overlap(max_nodes=0, tree=OK["context_lens"] + 4)  # not written
+    assert not overlap(num_seqs=0, context_lens=OK["slots"] + 4, new_lens=OK["slots"] + 4)  # not read
 
 
 @pytest.mark.parametrize("out", SIZE)

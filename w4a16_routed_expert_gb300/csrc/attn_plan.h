@@ -60,7 +60,7 @@ inline bool plan_overlaps_lengths(const Plan& p) {
   for (const int32_t* lengths : in)
     for (const auto& o : out) {
       const uintptr_t x = reinterpret_cast<uintptr_t>(lengths), y = reinterpret_cast<uintptr_t>(o.at);
-      if (lengths && o.at && o.n > 0 && x < y + (uintptr_t)o.n * 4 && y < x + (uintptr_t)B * 4) return true;
+      if (lengths && B > 0 && o.at && o.n > 0 && x < y + (uintptr_t)o.n * 4 && y < x + (uintptr_t)B * 4) return true;
     }
   return false;
 }
